@@ -217,6 +217,98 @@ mla_status mla_unabsorb_out(const mla_dims *dims, int batch, const void *z, cons
                             const void *W_O, int d_model, void *out, void *ws, size_t ws_bytes,
                             mla_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Prompts.  The calls below take many new tokens of several sequences at once,
+ * packed without padding: the tokens of sequence b are [cu[b], cu[b+1]) of the
+ * packed tensors, with cu an ascending int32 device array of batch + 1 offsets
+ * (sequences may be empty).  Packed rows outside [cu[0], cu[batch]) are neither
+ * read nor written.  Their supported shapes are those of the other calls, and
+ * with MLA_BF16 any n_heads <= 256 (heads shared out over devices) and any
+ * page_size >= 1.
+ *
+ * A layer's prompt, in the order of its calls ("解耦 RoPE（MLA 下）" §七
+ * forward_naive; "从零理解 MLA", 解耦 RoPE MLADecoupledRoPE.forward):
+ * mla_prompt_append writes the new rows [c ; k_R] and rotates the queries,
+ * mla_cache_gather reads all rows of the sequences (earlier chunks included)
+ * back in packed order, the caller expands them per head (K = W_UK c, V = W_UV c:
+ * plain matrix products), and mla_prompt_attn attends causally.  Per query, key
+ * and head this costs 2 (d_nope + d_rope + d_v) operations instead of the
+ * 2 (2 d_c + d_rope) of the absorbed form that decode uses. */
+
+/* A packed [tokens][heads][width] tensor whose element (t, h, i) is at
+ * ptr + t * token_stride + h * head_stride + i (strides in elements, so a slice
+ * of a wider tensor needs no copy).  Rows may not overlap: head_stride >= width,
+ * and token_stride >= width as far as there is more than one of them.  ptr is
+ * 16-byte aligned; with MLA_BF16 the strides are multiples of 8. */
+typedef struct {
+  void *ptr;
+  int64_t token_stride, head_stride;
+} mla_heads;
+
+/* Bytes of workspace the prompt calls need for `batch` sequences of n_tokens
+ * new tokens in all.  Initialise it with mla_workspace_init; device errors are
+ * read with mla_get_device_error.  Calls that may overlap (other streams, graphs
+ * that are replayed at the same time) need a workspace each. */
+size_t mla_prompt_workspace_size(const mla_dims *dims, int batch, int n_tokens);
+
+/* Cache append of packed rows ("解耦 RoPE（MLA 下）" §五 steps 2-3 for every
+ * token of a chunk).  Token t of sequence b has position
+ * p = ctx_lens[b] + t - cu[b]; with [x ; r] its row of `x`,
+ *   c = gamma * x / sqrt(mean(x^2) + rms_eps),  k_R = RoPE_p(r),
+ * and the row [c ; k_R], rounded once (int8 rows: quantised as described at
+ * MLA_CACHE_INT8, from a c held in 64 bits), is written to slot p of sequence b.
+ * With q_rope the same launch rotates the tokens' queries, q_out = RoPE_p(q_rope).
+ * x: [n_tokens][d_c + d_rope], the projections W_DKV h and W_KR h, rows x_stride
+ * elements apart (at least d_c + d_rope; MLA_BF16: a multiple of 8);
+ * gamma: [d_c]; ctx_lens: [batch] rows that the sequences already have, or NULL
+ * for none; q_rope, q_out: [n_tokens][n_heads][d_rope], both or neither (NULL);
+ * q_out may be q_rope itself, but may not overlap it otherwise.
+ * seq_lens is not read or changed, so it may be NULL in `cache`.  A row whose
+ * position has no page is not written and sets the error word (its queries are
+ * rotated).  Two tokens of one call may not map to the same slot. */
+mla_status mla_prompt_append(const mla_dims *dims, const mla_paged_cache *cache, int batch,
+                             int n_tokens, const void *x, int64_t x_stride, const void *gamma,
+                             const int32_t *cu_tokens, const int32_t *ctx_lens,
+                             const mla_heads *q_rope, const mla_heads *q_out, void *ws,
+                             size_t ws_bytes, mla_stream_t stream);
+
+/* Cache gather: rows first_rows[b] .. of every sequence, packed.
+ *   rows[t] = row (first_rows[b] + t - cu_rows[b]) of sequence b
+ * as d_c + d_rope values of dims->dtype; an int8 row as [q * s ; k_R], which bf16
+ * holds exactly.  rows: [n_rows][d_c + d_rope]; first_rows: [batch], or NULL for
+ * rows from 0 on.  seq_lens is not read (it may be NULL).  A row without a
+ * page is zeroed and sets the error word. */
+mla_status mla_cache_gather(const mla_dims *dims, const mla_paged_cache *cache, int batch,
+                            int n_rows, const int32_t *cu_rows, const int32_t *first_rows,
+                            void *rows, void *ws, size_t ws_bytes, mla_stream_t stream);
+
+/* Causal attention over packed sequences ("从零理解 MLA", 解耦 RoPE: score
+ * (q_C . k_C + q_R . k_R) / sqrt(d_head + d_r), the mask tril(diagonal = S - L)).
+ * Sequence b has lq = cu_q[b+1] - cu_q[b] queries and lk = cu_k[b+1] - cu_k[b]
+ * keys; its query i sees its keys j <= i + lk - lq (the last query sees them all):
+ *   out_i = sum_j softmax_j(scale * (q_nope_i . k_nope_j + q_rope_i . k_rope_j)) v_j,
+ *   lse_i = log sum_j exp(scale * (...))   (natural log),
+ * where head h reads the keys and values of head h / (n_heads / n_kv_heads): one
+ * key head per query head as MLA expands them, or grouped heads.  k_rope is
+ * shared by all heads.  A query that sees no key (lq > lk) gets out = 0,
+ * lse = -inf, and that is no error.
+ * q_nope: [n_q][n_heads][d_nope]; q_rope: [n_q][n_heads][d_rope], rotated;
+ * k_nope: [n_k][n_kv_heads][d_nope]; v: [n_k][n_kv_heads][d_v]; k_rope:
+ * [n_k][d_rope], rotated, rows k_rope_stride elements apart; out:
+ * [n_q][n_heads][d_v]; lse: [n_q][n_heads] fp32 or NULL.  k_nope, k_rope and v
+ * may be NULL when n_k is 0.  With MLA_BF16 the weights of a softmax are rounded
+ * to bf16 for the product with v (their sum is not); scores, maxima, sums and
+ * the accumulator are fp32.  Keys and values outside their own sequence never
+ * reach a result, whatever they hold; within a sequence an infinite or NaN v_j
+ * may make rows of its 128-key tile that come before it NaN as well.
+ * A sequence whose offsets do not ascend or leave [0, n_q] or [0, n_k] is
+ * skipped (its rows of out and lse keep what they held) and sets the error word. */
+mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, int n_kv_heads,
+                           const mla_heads *q_nope, const mla_heads *q_rope,
+                           const mla_heads *k_nope, const void *k_rope, int64_t k_rope_stride,
+                           const mla_heads *v, const int32_t *cu_q, const int32_t *cu_k, void *out,
+                           float *lse, void *ws, size_t ws_bytes, mla_stream_t stream);
+
 /* Decode attention without a caller-provided workspace.  The pages describe no
  * such variant: it exists for callers that cannot allocate device memory, e.g.
  * code whose device memory belongs entirely to another allocator (a

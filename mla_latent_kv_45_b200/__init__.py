@@ -7,6 +7,7 @@ input generator (``synth``).
 """
 
 from ._lib import (MLA_BF16, MLA_FP32, MLA_ROPE_HALF, MLA_ROPE_INTERLEAVED, Dims, MlaError,  # noqa: F401
-                   PagedCache, mla_absorb_q, mla_cache_append, mla_decode_attn,
-                   mla_get_device_error, mla_unabsorb_out, mla_workspace_init,
+                   PagedCache, mla_absorb_q, mla_cache_append, mla_cache_gather, mla_decode_attn,
+                   mla_get_device_error, mla_prompt_append, mla_prompt_attn,
+                   mla_prompt_workspace_size, mla_unabsorb_out, mla_workspace_init,
                    mla_workspace_size, status_string)

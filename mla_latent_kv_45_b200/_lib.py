@@ -29,7 +29,8 @@ STATUS = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED",
 
 EXPORTS = ("mla_workspace_size", "mla_workspace_init", "mla_cache_append", "mla_absorb_q",
            "mla_decode_attn", "mla_decode_attn_partial", "mla_merge_partials",
-           "mla_decode_attn_noalloc", "mla_unabsorb_out",
+           "mla_decode_attn_noalloc", "mla_unabsorb_out", "mla_prompt_workspace_size",
+           "mla_prompt_append", "mla_cache_gather", "mla_prompt_attn",
            "mla_noalloc_get_device_error", "mla_get_device_error", "mla_debug_absorb_timeout",
            "mla_status_string")
 
@@ -52,6 +53,11 @@ class _Cache(ctypes.Structure):
     _fields_ = [("pool", ctypes.c_void_p), ("num_pages", ctypes.c_int),
                 ("block_table", ctypes.c_void_p), ("max_pages_per_seq", ctypes.c_int),
                 ("seq_lens", ctypes.c_void_p)]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
 
 
 @dataclasses.dataclass
@@ -83,15 +89,16 @@ class PagedCache:
     """Mirror of ``mla_paged_cache`` holding the torch tensors.
 
     pool ``[num_pages, page_size, d_c + d_rope]``, block_table
-    ``[batch, max_pages_per_seq]`` int32, seq_lens ``[batch]`` int32.
+    ``[batch, max_pages_per_seq]`` int32, seq_lens ``[batch]`` int32 (None for
+    the calls that do not read it).
     """
     pool: torch.Tensor
     block_table: torch.Tensor
-    seq_lens: torch.Tensor
+    seq_lens: Optional[torch.Tensor]
 
     def c(self) -> _Cache:
         return _Cache(self.pool.data_ptr(), self.pool.shape[0], self.block_table.data_ptr(),
-                      self.block_table.shape[1], self.seq_lens.data_ptr())
+                      self.block_table.shape[1], _p(self.seq_lens))
 
 
 _lib = None
@@ -116,13 +123,21 @@ def lib() -> ctypes.CDLL:
         L.mla_merge_partials.argtypes = [pd, i, i, vp, vp, vp, vp, vp, vp]
         L.mla_decode_attn_noalloc.argtypes = [pd, pc, i, vp, vp, vp, i, vp]
         L.mla_unabsorb_out.argtypes = [pd, i, vp, vp, vp, i, vp, vp, sz, vp]
+        i64, ph = ctypes.c_int64, ctypes.POINTER(_Heads)
+        L.mla_prompt_workspace_size.argtypes = [pd, i, i]
+        L.mla_prompt_workspace_size.restype = sz
+        L.mla_prompt_append.argtypes = [pd, pc, i, i, vp, i64, vp, vp, vp, ph, ph, vp, sz, vp]
+        L.mla_cache_gather.argtypes = [pd, pc, i, i, vp, vp, vp, vp, sz, vp]
+        L.mla_prompt_attn.argtypes = [pd, i, i, i, i, ph, ph, ph, vp, i64, ph, vp, vp, vp, vp, vp,
+                                      sz, vp]
         L.mla_get_device_error.argtypes = [vp, vp]
         L.mla_noalloc_get_device_error.argtypes = [vp]
         L.mla_debug_absorb_timeout.argtypes = [i, ctypes.c_uint]
         L.mla_status_string.argtypes = [i]
         L.mla_status_string.restype = ctypes.c_char_p
         for name in EXPORTS:
-            if name not in ("mla_workspace_size", "mla_status_string"):
+            if name not in ("mla_workspace_size", "mla_prompt_workspace_size",
+                            "mla_status_string"):
                 getattr(L, name).restype = i
         _lib = L
     return _lib
@@ -215,6 +230,158 @@ def mla_unabsorb_out(dims: Dims, z, W_UV, W_O, out, ws: torch.Tensor, stream=Non
     _ok("mla_unabsorb_out", lib().mla_unabsorb_out(
         ctypes.byref(d), z.shape[0], _p(z), _p(W_UV), _p(W_O), d_model, _p(out), _p(ws),
         ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def _heads(fn: str, dims: Dims, t: torch.Tensor, name: str, heads: int, width: int) -> _Heads:
+    """The view of a [tokens, heads, width] tensor (any token and head strides)."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != width:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not [tokens, {heads}, {width}]")
+    _typed(fn, dims, t, name)
+    return _Heads(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _typed(fn: str, dims: Dims, t: torch.Tensor, name: str, last: bool = True):
+    if t.dtype != dims.torch_dtype:
+        raise ValueError(f"{fn}: {name} is {t.dtype}, not {dims.torch_dtype}")
+    if last and t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{fn}: the last axis of {name} is not contiguous")
+
+
+def _offsets(fn: str, t: Optional[torch.Tensor], name: str, n: Optional[int] = None):
+    if t is None:
+        return
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} is not a contiguous int32 vector")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{fn}: {name} has {t.numel()} entries, not {n}")
+
+
+def _same_device(fn: str, *tensors):
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1 or next(iter(devs)).type != "cuda":
+        raise ValueError(f"{fn}: tensors on {sorted(map(str, devs))}, not on one CUDA device")
+    return next(iter(devs))
+
+
+def _on(dev, stream):
+    """The stream to launch on (default: the device's current one), checked against the device."""
+    if stream is None:
+        return torch.cuda.current_stream(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+    return stream
+
+
+def _contiguous(fn: str, t: Optional[torch.Tensor], name: str, shape, dtype):
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} is {t.dtype} {tuple(t.shape)}, not a contiguous "
+                         f"{dtype} {tuple(shape)}")
+
+
+def _paged(fn: str, dims: Dims, cache: PagedCache, batch: int):
+    if dims.cache_format == MLA_CACHE_INT8:
+        width, dtype = MLA_INT8_ROW_BYTES, torch.uint8
+    else:
+        width, dtype = dims.d_c + dims.d_rope, dims.torch_dtype
+    _contiguous(fn, cache.pool, "pool", (cache.pool.shape[0], dims.page_size, width), dtype)
+    if cache.block_table.dim() != 2 or cache.block_table.shape[0] != batch:
+        raise ValueError(f"{fn}: block_table has shape {tuple(cache.block_table.shape)}, "
+                         f"not [{batch}, max_pages]")
+    _contiguous(fn, cache.block_table, "block_table", cache.block_table.shape, torch.int32)
+
+
+def mla_prompt_workspace_size(dims: Dims, batch: int, n_tokens: int) -> int:
+    d = dims.c()
+    return int(lib().mla_prompt_workspace_size(ctypes.byref(d), batch, n_tokens))
+
+
+def mla_prompt_append(dims: Dims, cache: PagedCache, x, gamma, cu_tokens, ctx_lens=None,
+                      q_rope=None, q_out=None, ws: torch.Tensor = None, stream=None):
+    """Packed rows into the paged cache, normalised and rotated, and the queries rotated.
+
+    x ``[tokens, d_c + d_rope]`` (any row stride), cu_tokens ``[batch + 1]`` int32,
+    ctx_lens ``[batch]`` int32 or None, q_rope and q_out ``[tokens, n_heads,
+    d_rope]`` (any token and head strides; q_out may be q_rope) or None.
+    """
+    fn = "mla_prompt_append"
+    _offsets(fn, cu_tokens, "cu_tokens")
+    batch = cu_tokens.numel() - 1
+    _offsets(fn, ctx_lens, "ctx_lens", batch)
+    _paged(fn, dims, cache, batch)
+    if x.dim() != 2 or x.shape[1] != dims.d_c + dims.d_rope:
+        raise ValueError(f"{fn}: x has shape {tuple(x.shape)}, not [tokens, {dims.d_c + dims.d_rope}]")
+    _typed(fn, dims, x, "x")
+    _contiguous(fn, gamma, "gamma", (dims.d_c,), dims.torch_dtype)
+    if (q_rope is None) != (q_out is None):
+        raise ValueError(f"{fn}: q_rope and q_out go together")
+    dev = _same_device(fn, x, gamma, cu_tokens, ctx_lens, cache.pool, cache.block_table, q_rope,
+                       q_out, ws)
+    q = qo = None
+    if q_rope is not None:
+        if q_rope.shape[0] != x.shape[0] or q_out.shape[0] != x.shape[0]:
+            raise ValueError(f"{fn}: x, q_rope and q_out differ in their number of tokens")
+        q = ctypes.byref(_heads(fn, dims, q_rope, "q_rope", dims.n_heads, dims.d_rope))
+        qo = ctypes.byref(_heads(fn, dims, q_out, "q_out", dims.n_heads, dims.d_rope))
+    d, c = dims.c(), cache.c()
+    with torch.cuda.device(dev):
+        _ok(fn, lib().mla_prompt_append(
+            ctypes.byref(d), ctypes.byref(c), batch, x.shape[0], _p(x), x.stride(0), _p(gamma),
+            _p(cu_tokens), _p(ctx_lens), q, qo, _p(ws), ws.numel() * ws.element_size(),
+            _stream(_on(dev, stream))))
+
+
+def mla_cache_gather(dims: Dims, cache: PagedCache, cu_rows, first_rows, rows,
+                     ws: torch.Tensor = None, stream=None):
+    """rows ``[n, d_c + d_rope]``: each sequence's cached rows from first_rows[b] (None: 0) on,
+    packed at cu_rows ``[batch + 1]``; int8 rows come back as the values they hold."""
+    fn = "mla_cache_gather"
+    _offsets(fn, cu_rows, "cu_rows")
+    batch = cu_rows.numel() - 1
+    _offsets(fn, first_rows, "first_rows", batch)
+    _paged(fn, dims, cache, batch)
+    _contiguous(fn, rows, "rows", (rows.shape[0], dims.d_c + dims.d_rope), dims.torch_dtype)
+    dev = _same_device(fn, cu_rows, first_rows, rows, cache.pool, cache.block_table, ws)
+    d, c = dims.c(), cache.c()
+    with torch.cuda.device(dev):
+        _ok(fn, lib().mla_cache_gather(
+            ctypes.byref(d), ctypes.byref(c), batch, rows.shape[0], _p(cu_rows), _p(first_rows),
+            _p(rows), _p(ws), ws.numel() * ws.element_size(), _stream(_on(dev, stream))))
+
+
+def mla_prompt_attn(dims: Dims, q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, out, lse=None,
+                    ws: torch.Tensor = None, stream=None):
+    """Causal attention over packed sequences.
+
+    q_nope ``[n_q, n_heads, d_nope]``, q_rope ``[n_q, n_heads, d_rope]``, k_nope
+    ``[n_k, n_kv_heads, d_nope]``, v ``[n_k, n_kv_heads, d_v]`` (any token and
+    head strides), k_rope ``[n_k, d_rope]`` (any row stride), cu_q and cu_k
+    ``[batch + 1]`` int32, out ``[n_q, n_heads, d_v]``, lse ``[n_q, n_heads]``
+    fp32 or None.
+    """
+    fn = "mla_prompt_attn"
+    _offsets(fn, cu_q, "cu_q")
+    _offsets(fn, cu_k, "cu_k", cu_q.numel())
+    n_q, n_k, n_kv = q_nope.shape[0], k_nope.shape[0], k_nope.shape[1]
+    qn = _heads(fn, dims, q_nope, "q_nope", dims.n_heads, dims.d_nope)
+    qr = _heads(fn, dims, q_rope, "q_rope", dims.n_heads, dims.d_rope)
+    kn = _heads(fn, dims, k_nope, "k_nope", n_kv, dims.d_nope)
+    vv = _heads(fn, dims, v, "v", n_kv, dims.d_v)
+    if k_rope.dim() != 2 or k_rope.shape[1] != dims.d_rope:
+        raise ValueError(f"{fn}: k_rope has shape {tuple(k_rope.shape)}, not [n_k, {dims.d_rope}]")
+    _typed(fn, dims, k_rope, "k_rope")
+    if q_rope.shape[0] != n_q or k_rope.shape[0] != n_k or v.shape[0] != n_k:
+        raise ValueError(f"{fn}: the queries or the keys and values differ in their number of tokens")
+    _contiguous(fn, out, "out", (n_q, dims.n_heads, dims.d_v), dims.torch_dtype)
+    _contiguous(fn, lse, "lse", (n_q, dims.n_heads), torch.float32)
+    dev = _same_device(fn, q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, out, lse, ws)
+    d = dims.c()
+    with torch.cuda.device(dev):
+        _ok(fn, lib().mla_prompt_attn(
+            ctypes.byref(d), cu_q.numel() - 1, n_q, n_k, n_kv, ctypes.byref(qn), ctypes.byref(qr),
+            ctypes.byref(kn), _p(k_rope), k_rope.stride(0), ctypes.byref(vv), _p(cu_q), _p(cu_k),
+            _p(out), _p(lse), _p(ws), ws.numel() * ws.element_size(), _stream(_on(dev, stream))))
 
 
 def mla_noalloc_get_device_error(stream=None) -> int:

@@ -5,11 +5,13 @@
 
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 
 #include <mutex>
 
 #include <cuda_runtime.h>
 
+#include "common.cuh"
 #include "mla.h"
 
 namespace mla {
@@ -45,6 +47,18 @@ inline mla_status check_dims(const mla_dims *d) {
   return MLA_OK;
 }
 
+// Sizes accepted by the prompt calls: as check_dims, but in bf16 any number of
+// heads up to 256 (a layer's heads may be shared out over devices) and any page size.
+inline mla_status check_prompt_dims(const mla_dims *d) {
+  if (!d) return MLA_ERR_INVALID_ARG;
+  mla_dims t = *d;
+  if (t.dtype == MLA_BF16 && t.n_heads >= 1 && t.n_heads <= 256 && t.page_size >= 1) {
+    t.n_heads = 128;
+    t.page_size = 64;
+  }
+  return check_dims(&t);
+}
+
 inline mla_status check_cache(const mla_paged_cache *c) {
   if (!c || !c->pool || !c->block_table || c->num_pages < 1 || c->max_pages_per_seq < 1)
     return MLA_ERR_INVALID_ARG;
@@ -72,6 +86,16 @@ inline mla_status check_attn_args(const mla_dims *dims, const mla_paged_cache *c
 inline float softmax_scale(const mla_dims &d) {
   return d.softmax_scale > 0 ? (float)d.softmax_scale
                              : (float)(1.0 / sqrt((double)(d.d_nope + d.d_rope)));
+}
+
+// Frequencies theta_i = rope_base^(-2i/d_rope) in fp64 and the pair layout.
+inline RopeParams rope_params(const mla_dims &d) {
+  RopeParams rp;
+  memset(&rp, 0, sizeof(rp));
+  rp.d_rope = d.d_rope;
+  rp.half = d.rope_layout == MLA_ROPE_HALF;
+  for (int i = 0; i < d.d_rope / 2; ++i) rp.theta[i] = pow(d.rope_base, -2.0 * i / d.d_rope);
+  return rp;
 }
 
 // Raises a kernel's dynamic shared-memory limit once per device (the attribute

@@ -18,6 +18,7 @@ using namespace mla;
 using api::aligned16;
 using api::check_cache;
 using api::check_dims;
+using api::rope_params;
 using api::softmax_scale;
 using bf16 = __nv_bfloat16;
 
@@ -76,15 +77,6 @@ mla_status check_width(const mla_dims *d, int w) {
   if (w < 1) return MLA_ERR_INVALID_ARG;
   if (d->dtype == MLA_BF16 && (w % 64)) return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
-}
-
-RopeParams rope_params(const mla_dims &d) {
-  RopeParams rp;
-  memset(&rp, 0, sizeof(rp));
-  rp.d_rope = d.d_rope;
-  rp.half = d.rope_layout == MLA_ROPE_HALF;
-  for (int i = 0; i < d.d_rope / 2; ++i) rp.theta[i] = pow(d.rope_base, -2.0 * i / d.d_rope);
-  return rp;
 }
 
 char *at(void *ws, size_t off) { return static_cast<char *>(ws) + off; }

@@ -1,0 +1,211 @@
+// Host side of the prompt calls declared in include/mla.h: argument checks,
+// workspace layout and dispatch.  Nothing here allocates or synchronises.
+#include <cuda_runtime.h>
+
+#include "api_checks.h"
+#include "common.cuh"
+#include "mla.h"
+#include "prompt.h"
+
+namespace {
+
+using namespace mla;
+using api::aligned16;
+using api::aligned4;
+
+#define MLA_TRY(x)                 \
+  do {                             \
+    mla_status st_ = (x);          \
+    if (st_ != MLA_OK) return st_; \
+  } while (0)
+
+mla_status cuda_ok(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
+
+int tile_rows(const mla_dims &d) {
+  (void)d;
+  return kPromptTileSimt;
+}
+
+// The error word and the plan header share the first 256 bytes (the part that
+// mla_workspace_init clears); the plan's items follow.
+constexpr size_t kItemsAt = 256, kHeaderAt = 64;
+
+size_t prompt_ws_bytes(const mla_dims &d, int batch, int n_tokens) {
+  return kItemsAt + sizeof(PromptItem) * (size_t)prompt_max_items(n_tokens, batch, tile_rows(d));
+}
+
+mla_status check_ws(const void *ws, size_t ws_bytes, size_t need) {
+  if (!ws) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(ws)) return MLA_ERR_ALIGNMENT;
+  return ws_bytes < need ? MLA_ERR_WORKSPACE : MLA_OK;
+}
+
+int *err_of(void *ws) { return static_cast<int *>(ws); }
+
+mla_status check_heads(const mla_dims &d, const mla_heads *h, int tokens, int heads, int width) {
+  if (!h || !h->ptr) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(h->ptr)) return MLA_ERR_ALIGNMENT;
+  if (heads > 1 && h->head_stride < width) return MLA_ERR_INVALID_ARG;
+  if (tokens > 1 && h->token_stride < width) return MLA_ERR_INVALID_ARG;
+  if (d.dtype == MLA_BF16 &&
+      ((heads > 1 && h->head_stride % 8) || (tokens > 1 && h->token_stride % 8)))
+    return MLA_ERR_ALIGNMENT;
+  return MLA_OK;
+}
+
+// Strides of an extent of one are not used; the kernels get a harmless value.
+HeadsView view(const mla_heads *h, int tokens, int heads, int width) {
+  HeadsView v{};
+  if (!h) return v;
+  v.ptr = h->ptr;
+  v.token = tokens > 1 ? h->token_stride : width;
+  v.head = heads > 1 ? h->head_stride : width;
+  return v;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mla_prompt_workspace_size(const mla_dims *dims, int batch, int n_tokens) {
+  if (api::check_prompt_dims(dims) != MLA_OK || batch < 1 || n_tokens < 0) return 0;
+  return prompt_ws_bytes(*dims, batch, n_tokens);
+}
+
+mla_status mla_prompt_append(const mla_dims *dims, const mla_paged_cache *cache, int batch,
+                             int n_tokens, const void *x, int64_t x_stride, const void *gamma,
+                             const int32_t *cu_tokens, const int32_t *ctx_lens,
+                             const mla_heads *q_rope, const mla_heads *q_out, void *ws,
+                             size_t ws_bytes, mla_stream_t stream) {
+  MLA_TRY(api::check_prompt_dims(dims));
+  MLA_TRY(api::check_cache(cache));
+  const mla_dims &d = *dims;
+  if (batch < 1 || n_tokens < 0 || !gamma || !cu_tokens || !q_rope != !q_out)
+    return MLA_ERR_INVALID_ARG;
+  MLA_TRY(check_ws(ws, ws_bytes, kItemsAt));
+  if (!aligned16(gamma) || !aligned4(cu_tokens) || !aligned4(ctx_lens)) return MLA_ERR_ALIGNMENT;
+  if (n_tokens == 0) return MLA_OK;
+  if (!x || (n_tokens > 1 && x_stride < d.d_c + d.d_rope)) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(x) || (d.dtype == MLA_BF16 && n_tokens > 1 && x_stride % 8))
+    return MLA_ERR_ALIGNMENT;
+  if (q_rope) {
+    MLA_TRY(check_heads(d, q_rope, n_tokens, d.n_heads, d.d_rope));
+    MLA_TRY(check_heads(d, q_out, n_tokens, d.n_heads, d.d_rope));
+  }
+  PromptAppendArgs a{};
+  a.x = x;
+  a.x_stride = x_stride;
+  a.gamma = gamma;
+  a.cu = cu_tokens;
+  a.ctx = ctx_lens;
+  a.batch = batch;
+  a.n_tokens = n_tokens;
+  a.n_heads = d.n_heads;
+  a.d_c = d.d_c;
+  a.q = view(q_rope, n_tokens, d.n_heads, d.d_rope);
+  a.q_out = view(q_out, n_tokens, d.n_heads, d.d_rope);
+  a.pool = cache->pool;
+  a.block_table = cache->block_table;
+  a.num_pages = cache->num_pages;
+  a.page_size = d.page_size;
+  a.max_pages = cache->max_pages_per_seq;
+  a.eps = d.rms_eps;
+  a.err = err_of(ws);
+  const RopeParams rp = api::rope_params(d);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (d.dtype == MLA_FP32) return cuda_ok(launch_prompt_append_f32(a, rp, s));
+  return cuda_ok(launch_prompt_append_bf16(a, rp, d.cache_format == MLA_CACHE_INT8, s));
+}
+
+mla_status mla_cache_gather(const mla_dims *dims, const mla_paged_cache *cache, int batch,
+                            int n_rows, const int32_t *cu_rows, const int32_t *first_rows,
+                            void *rows, void *ws, size_t ws_bytes, mla_stream_t stream) {
+  MLA_TRY(api::check_prompt_dims(dims));
+  MLA_TRY(api::check_cache(cache));
+  const mla_dims &d = *dims;
+  if (batch < 1 || n_rows < 0 || !cu_rows) return MLA_ERR_INVALID_ARG;
+  MLA_TRY(check_ws(ws, ws_bytes, kItemsAt));
+  if (!aligned4(cu_rows) || !aligned4(first_rows)) return MLA_ERR_ALIGNMENT;
+  if (n_rows == 0) return MLA_OK;
+  if (!rows) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(rows)) return MLA_ERR_ALIGNMENT;
+  GatherArgs a{};
+  a.pool = cache->pool;
+  a.block_table = cache->block_table;
+  a.cu = cu_rows;
+  a.first = first_rows;
+  a.batch = batch;
+  a.n_rows = n_rows;
+  a.num_pages = cache->num_pages;
+  a.page_size = d.page_size;
+  a.max_pages = cache->max_pages_per_seq;
+  a.rows = rows;
+  a.err = err_of(ws);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (d.dtype == MLA_FP32) return cuda_ok(launch_gather_f32(a, d.d_c + d.d_rope, s));
+  return cuda_ok(launch_gather_bf16(a, d.cache_format == MLA_CACHE_INT8, s));
+}
+
+mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, int n_kv_heads,
+                           const mla_heads *q_nope, const mla_heads *q_rope,
+                           const mla_heads *k_nope, const void *k_rope, int64_t k_rope_stride,
+                           const mla_heads *v, const int32_t *cu_q, const int32_t *cu_k, void *out,
+                           float *lse, void *ws, size_t ws_bytes, mla_stream_t stream) {
+  MLA_TRY(api::check_prompt_dims(dims));
+  const mla_dims &d = *dims;
+  if (batch < 1 || n_q < 0 || n_k < 0 || n_kv_heads < 1 || n_kv_heads > d.n_heads || !cu_q || !cu_k)
+    return MLA_ERR_INVALID_ARG;
+  if (d.n_heads % n_kv_heads) return MLA_ERR_INVALID_ARG;
+  if (!aligned4(cu_q) || !aligned4(cu_k) || !aligned4(lse)) return MLA_ERR_ALIGNMENT;
+  MLA_TRY(check_ws(ws, ws_bytes, prompt_ws_bytes(d, batch, n_q)));
+  if (n_q == 0) return MLA_OK;
+  if (!out) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(out)) return MLA_ERR_ALIGNMENT;
+  MLA_TRY(check_heads(d, q_nope, n_q, d.n_heads, d.d_nope));
+  MLA_TRY(check_heads(d, q_rope, n_q, d.n_heads, d.d_rope));
+  if (n_k > 0) {
+    MLA_TRY(check_heads(d, k_nope, n_k, n_kv_heads, d.d_nope));
+    MLA_TRY(check_heads(d, v, n_k, n_kv_heads, d.d_v));
+    const mla_heads kr{const_cast<void *>(k_rope), k_rope_stride, 0};
+    MLA_TRY(check_heads(d, &kr, n_k, 1, d.d_rope));
+  }
+  cudaStream_t s = (cudaStream_t)stream;
+  PromptPlanArgs pa{};
+  pa.cu_q = cu_q;
+  pa.cu_k = cu_k;
+  pa.batch = batch;
+  pa.n_q = n_q;
+  pa.n_k = n_k;
+  pa.tile = tile_rows(d);
+  pa.hdr = reinterpret_cast<PromptPlanHeader *>(static_cast<char *>(ws) + kHeaderAt);
+  pa.items = reinterpret_cast<PromptItem *>(static_cast<char *>(ws) + kItemsAt);
+  pa.err = err_of(ws);
+  MLA_TRY(cuda_ok(launch_prompt_plan(pa, s)));
+  PromptAttnArgs a{};
+  a.q_nope = view(q_nope, n_q, d.n_heads, d.d_nope);
+  a.q_rope = view(q_rope, n_q, d.n_heads, d.d_rope);
+  if (n_k > 0) {
+    a.k_nope = view(k_nope, n_k, n_kv_heads, d.d_nope);
+    a.v = view(v, n_k, n_kv_heads, d.d_v);
+    a.k_rope = k_rope;
+    a.k_rope_stride = n_k > 1 ? k_rope_stride : d.d_rope;
+  }
+  a.n_q = n_q;
+  a.n_k = n_k;
+  a.n_heads = d.n_heads;
+  a.n_kv_heads = n_kv_heads;
+  a.d_nope = d.d_nope;
+  a.d_rope = d.d_rope;
+  a.d_v = d.d_v;
+  a.max_items = prompt_max_items(n_q, batch, pa.tile);
+  a.scale = api::softmax_scale(d);
+  a.hdr = pa.hdr;
+  a.items = pa.items;
+  a.out = out;
+  a.lse = lse;
+  a.err = pa.err;
+  if (d.dtype == MLA_FP32) return cuda_ok(launch_prompt_attn_simt<float>(a, s));
+  return cuda_ok(launch_prompt_attn_simt<__nv_bfloat16>(a, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,597 @@
+// Prompt operators on CUDA cores: cache append of packed rows (RMSNorm, RoPE,
+// paged write, query rotation), cache gather, the plan of the packed
+// attention, and the fp32 validation attention.
+#include "api_checks.h"
+#include "common.cuh"
+#include "prompt.h"
+
+namespace mla {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+// The sequence b with cu[b] <= t < cu[b + 1], by one warp (every lane gets the
+// result): the number of cu[1 .. batch] that are <= t, found 32 probes at a
+// time.  -1 when no sequence holds t; offsets that do not ascend end up there
+// or at a sequence that does hold t.
+__device__ __forceinline__ int warp_find_seq(const int32_t *cu, int batch, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = batch;  // the count is in [lo, lo + n]
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int at = lo + min(n, (lane + 1) * step);
+    const unsigned below = __ballot_sync(0xffffffffu, cu[at] <= t);
+    const int k = __popc(below);  // lanes whose probe is <= t
+    if (step == 1) {
+      lo += min(n, k);
+      break;
+    }
+    const int skip = min(n, k * step);
+    lo += skip;
+    n = min(n - skip, step - 1);
+  }
+  if (lo >= batch || t < cu[lo] || t >= cu[lo + 1]) return -1;
+  return lo;
+}
+
+// The page and slot of row `pos` of sequence b; page -1 when out of range.
+__device__ __forceinline__ int page_of(const int32_t *table, int max_pages, int num_pages,
+                                       int page_size, int b, long pos) {
+  if (pos < 0 || pos >= (long)max_pages * page_size) return -1;
+  const int page = table[(long)b * max_pages + pos / page_size];
+  return page >= 0 && page < num_pages ? page : -1;
+}
+
+__device__ __forceinline__ void unpack8(const uint4 &u, float *f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float *f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&v);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ---------------------------------------------------------------------------
+// Cache append of packed rows
+// ---------------------------------------------------------------------------
+
+__global__ void prompt_append_f32(PromptAppendArgs a, RopeParams rp) {
+  __shared__ float cs[64], sn[64], red[32];
+  __shared__ float inv_rms;
+  grid_dep_wait();
+  const int t = blockIdx.x, half = rp.d_rope / 2, row = a.d_c + rp.d_rope;
+  const int b = warp_find_seq(a.cu, a.batch, t);
+  if (b < 0) {
+    // tokens outside [cu[0], cu[batch]) are not there; one inside that no
+    // sequence holds means offsets that do not ascend
+    if (threadIdx.x == 0 && t >= a.cu[0] && t < a.cu[a.batch]) set_error(a.err, kErrRange);
+    return;
+  }
+  const long pos = (long)(a.ctx ? a.ctx[b] : 0) + (t - a.cu[b]);
+  const int page = page_of(a.block_table, a.max_pages, a.num_pages, a.page_size, b, pos);
+  if (pos < 0 || pos > 0x7fffffffL) {
+    if (threadIdx.x == 0) set_error(a.err, kErrRange);
+    return;
+  }
+  for (int i = threadIdx.x; i < half; i += blockDim.x)
+    rope_cos_sin((int)pos, rp.theta[i], cs[i], sn[i]);
+  const float *x = static_cast<const float *>(a.x) + t * a.x_stride;
+  float ss = 0.f;
+  for (int i = threadIdx.x; i < a.d_c; i += blockDim.x) ss += x[i] * x[i];
+  ss = warp_sum(ss);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = ss;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const float v = warp_sum(threadIdx.x < (blockDim.x >> 5) ? red[threadIdx.x] : 0.f);
+    if (threadIdx.x == 0) inv_rms = 1.0f / sqrtf(v / (float)a.d_c + (float)a.eps);
+  }
+  __syncthreads();
+  if (page < 0) {
+    if (threadIdx.x == 0) set_error(a.err, kErrRange);
+  } else {
+    float *dst = static_cast<float *>(a.pool) + ((long)page * a.page_size + pos % a.page_size) * row;
+    const float *gamma = static_cast<const float *>(a.gamma);
+    for (int i = threadIdx.x; i < a.d_c; i += blockDim.x) dst[i] = gamma[i] * (x[i] * inv_rms);
+    for (int i = threadIdx.x; i < half; i += blockDim.x) {
+      int j0, j1;
+      rope_idx(rp, i, j0, j1);
+      float x0 = x[a.d_c + j0], x1 = x[a.d_c + j1];
+      rope_rotate(cs[i], sn[i], x0, x1);
+      dst[a.d_c + j0] = x0;
+      dst[a.d_c + j1] = x1;
+    }
+  }
+  if (!a.q.ptr) return;
+  const float *q = static_cast<const float *>(a.q.ptr) + t * a.q.token;
+  float *qo = static_cast<float *>(const_cast<void *>(a.q_out.ptr)) + t * a.q_out.token;
+  for (int k = threadIdx.x; k < a.n_heads * half; k += blockDim.x) {
+    const int h = k / half, i = k % half;
+    int j0, j1;
+    rope_idx(rp, i, j0, j1);
+    float x0 = q[h * a.q.head + j0], x1 = q[h * a.q.head + j1];
+    rope_rotate(cs[i], sn[i], x0, x1);
+    qo[h * a.q_out.head + j0] = x0;
+    qo[h * a.q_out.head + j1] = x1;
+  }
+}
+
+constexpr int kSlab = 16;  // heads a warp rotates per round: 2 units of 8 pairs a lane
+
+// A token is the work of `group` warps: the last one normalises, rotates and
+// writes the cache row, the others rotate the heads.  Every warp finds its
+// token's sequence and evaluates the 32 angles (one a lane) by itself, so
+// nothing is shared between warps and nothing waits.
+//
+// A unit is 8 rotation pairs = two 16-byte vectors of a 64-wide head:
+// interleaved pairs (vectors 2u, 2u + 1) or split halves (vectors u, u + 4).  Lane l
+// handles unit l % 4, so its 8 cosines and sines stay in registers for all heads.
+template <bool kI8>
+__global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ RopeParams rp,
+                                   int group) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * (blockDim.x / 32 / group) + warp / group;
+  const int role = warp % group;
+  grid_dep_wait();
+  if (t >= a.n_tokens) return;
+  const int b = warp_find_seq(a.cu, a.batch, t);
+  if (b < 0) {
+    if (lane == 0 && t >= a.cu[0] && t < a.cu[a.batch]) set_error(a.err, kErrRange);
+    return;
+  }
+  const long pos = (long)(a.ctx ? a.ctx[b] : 0) + (t - a.cu[b]);
+  if (pos < 0 || pos > 0x7fffffffL) {
+    if (lane == 0) set_error(a.err, kErrRange);
+    return;
+  }
+  float cf, sf;
+  rope_cos_sin((int)pos, rp.theta[lane], cf, sf);
+  const int u = lane & 3;
+  float cs[8], sn[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    cs[i] = __shfl_sync(0xffffffffu, cf, 8 * u + i);
+    sn[i] = __shfl_sync(0xffffffffu, sf, 8 * u + i);
+  }
+  const int v0 = rp.half ? u : 2 * u, v1 = rp.half ? u + 4 : 2 * u + 1;
+  auto turn = [&](uint4 &p, uint4 &r) {
+    float f[16];
+    unpack8(p, f);
+    unpack8(r, f + 8);
+    if (rp.half) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rope_rotate(cs[i], sn[i], f[i], f[8 + i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rope_rotate(cs[i], sn[i], f[2 * i], f[2 * i + 1]);
+    }
+    p = pack8(f);
+    r = pack8(f + 8);
+  };
+
+  if (role < group - 1) {
+    const bf16 *q = static_cast<const bf16 *>(a.q.ptr) + t * a.q.token;
+    bf16 *qo = static_cast<bf16 *>(const_cast<void *>(a.q_out.ptr)) + t * a.q_out.token;
+    for (int h0 = role * kSlab; h0 < a.n_heads; h0 += (group - 1) * kSlab) {
+      uint4 p[2], r[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int h = h0 + 8 * k + (lane >> 2);
+        if (h < a.n_heads) {
+          const uint4 *src = reinterpret_cast<const uint4 *>(q + h * a.q.head);
+          p[k] = src[v0];
+          r[k] = src[v1];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int h = h0 + 8 * k + (lane >> 2);
+        if (h < a.n_heads) {
+          turn(p[k], r[k]);
+          uint4 *dst = reinterpret_cast<uint4 *>(qo + h * a.q_out.head);
+          dst[v0] = p[k];
+          dst[v1] = r[k];
+        }
+      }
+    }
+    return;
+  }
+
+  // the cache row: lane l holds latent values [16 l, 16 l + 16), lanes 0..3 also
+  // one unit of k_R
+  const int page = page_of(a.block_table, a.max_pages, a.num_pages, a.page_size, b, pos);
+  if (page < 0) {
+    if (lane == 0) set_error(a.err, kErrRange);
+    return;
+  }
+  const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(a.x) + t * a.x_stride);
+  const uint4 *g = static_cast<const uint4 *>(a.gamma);
+  float c[16], gm[16];
+  unpack8(x[2 * lane], c);
+  unpack8(x[2 * lane + 1], c + 8);
+  unpack8(g[2 * lane], gm);
+  unpack8(g[2 * lane + 1], gm + 8);
+  uint4 kp = make_uint4(0, 0, 0, 0), kr = kp;
+  if (lane < 4) {
+    kp = x[64 + v0];
+    kr = x[64 + v1];
+    turn(kp, kr);
+  }
+  const long slot = (long)page * a.page_size + pos % a.page_size;
+  if (!kI8) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ss += c[i] * c[i];
+    const float inv = 1.0f / sqrtf(warp_sum(ss) / 512.f + (float)a.eps);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) c[i] = gm[i] * (c[i] * inv);
+    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<bf16 *>(a.pool) + slot * 576);
+    dst[2 * lane] = pack8(c);
+    dst[2 * lane + 1] = pack8(c + 8);
+    if (lane < 4) {
+      dst[64 + v0] = kp;
+      dst[64 + v1] = kr;
+    }
+  } else {
+    // In 64 bits: a code is a rounding of c / 2^e, and a 32-bit c next to a
+    // border between two codes would fall on the wrong side of it.  About 50
+    // such operations a lane, far below the time the row's bytes take.
+    double ss = 0.0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ss += (double)c[i] * (double)c[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const double inv = 1.0 / sqrt(ss / 512.0 + a.eps);
+    double d[16], am = 0.0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      d[i] = (double)gm[i] * (double)c[i] * inv;
+      am = fmax(am, fabs(d[i]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) am = fmax(am, __shfl_xor_sync(0xffffffffu, am, o));
+    // am in [2^k, 2^(k+1)): 127 * 2^(k-6) = 1.98 * 2^k, so e is k - 6 or k - 5
+    int e = 0;
+    if (am > 0.0) {
+      e = ilogb(am) - 6;
+      if (am > ldexp(127.0, e)) ++e;
+    }
+    const double inv_s = ldexp(1.0, -e);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int q = max(-127, min(127, __double2int_rn(d[i] * inv_s)));
+      w[i >> 2] |= (uint32_t)(q & 255) << (8 * (i & 3));
+    }
+    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.pool) + slot * 656);
+    dst[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (lane < 4) {
+      dst[32 + v0] = kp;
+      dst[32 + v1] = kr;
+    }
+    if (lane == 4) dst[40] = make_uint4(__float_as_uint(ldexpf(1.f, e)), 0, 0, 0);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Cache gather: packed rows out of the pages
+// ---------------------------------------------------------------------------
+
+// Source row (page * page_size + slot) of packed row t by one warp: -1 when t
+// belongs to no sequence, -2 when its place in the cache is out of range.
+__device__ __forceinline__ long gather_source(const GatherArgs &a, int t) {
+  const int b = warp_find_seq(a.cu, a.batch, t);
+  if (b < 0) return t >= a.cu[0] && t < a.cu[a.batch] ? -2 : -1;
+  const long pos = (long)(a.first ? a.first[b] : 0) + (t - a.cu[b]);
+  const int page = page_of(a.block_table, a.max_pages, a.num_pages, a.page_size, b, pos);
+  return page < 0 ? -2 : (long)page * a.page_size + pos % a.page_size;
+}
+
+// One warp a row.  A row without a place in the cache is zeroed.
+__global__ void gather_f32(GatherArgs a, int row) {
+  const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  grid_dep_wait();
+  if (t >= a.n_rows) return;
+  const long src = gather_source(a, t);
+  if (src == -1) return;
+  if (src < 0 && lane == 0) set_error(a.err, kErrRange);
+  const float *p = static_cast<const float *>(a.pool) + (src < 0 ? 0 : src) * row;
+  float *o = static_cast<float *>(a.rows) + (long)t * row;
+  for (int i = lane; i < row; i += 32) o[i] = src < 0 ? 0.f : p[i];
+}
+
+// 16 int8 codes times the power-of-two scale s, as 16 bf16 values (exact).
+__device__ __forceinline__ void codes16(const uint4 &in, float s, uint4 &lo, uint4 &hi) {
+  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+  float f[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    f[i] = (float)static_cast<int8_t>(w[i >> 2] >> (8 * (i & 3))) * s;
+  lo = pack8(f);
+  hi = pack8(f + 8);
+}
+
+template <bool kI8>
+__global__ void gather_bf16(GatherArgs a) {
+  const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  grid_dep_wait();
+  if (t >= a.n_rows) return;
+  const long src = gather_source(a, t);
+  if (src == -1) return;
+  uint4 *o = reinterpret_cast<uint4 *>(static_cast<bf16 *>(a.rows) + (long)t * 576);
+  if (src < 0) {
+    if (lane == 0) set_error(a.err, kErrRange);
+    for (int i = lane; i < 72; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  if (kI8) {
+    const uint8_t *p = static_cast<const uint8_t *>(a.pool) + src * 656;
+    const uint4 *v = reinterpret_cast<const uint4 *>(p);
+    const uint4 codes = v[lane];
+    const uint4 kr = lane < 8 ? v[32 + lane] : make_uint4(0, 0, 0, 0);
+    const float s = *reinterpret_cast<const float *>(p + 640);
+    uint4 lo, hi;
+    codes16(codes, s, lo, hi);
+    o[2 * lane] = lo;
+    o[2 * lane + 1] = hi;
+    if (lane < 8) o[64 + lane] = kr;
+  } else {
+    const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(a.pool) + src * 576);
+    const uint4 x = v[lane], y = v[32 + lane];
+    if (lane < 8) o[64 + lane] = v[64 + lane];
+    o[lane] = x;
+    o[32 + lane] = y;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Plan of the packed attention: the query blocks, most keys first
+// ---------------------------------------------------------------------------
+//
+// Blocks are laid out by a counting sort on the keys that their last row sees,
+// in kBins equal steps, so that the blocks which take longest start first and
+// the short ones fill the end.
+constexpr int kBins = 1024;
+
+__device__ __forceinline__ bool seq_range(const PromptPlanArgs &a, int b, int &q0, int &lq, int &k0,
+                                          int &lk) {
+  q0 = a.cu_q[b];
+  const int q1 = a.cu_q[b + 1];
+  k0 = a.cu_k[b];
+  const int k1 = a.cu_k[b + 1];
+  lq = q1 - q0;
+  lk = k1 - k0;
+  return q0 >= 0 && q1 >= q0 && q1 <= a.n_q && k0 >= 0 && k1 >= k0 && k1 <= a.n_k;
+}
+
+__global__ void __launch_bounds__(1024) prompt_plan_kernel(PromptPlanArgs a) {
+  __shared__ int bins[kBins], warp_tot[32], top_s;
+  const int tid = threadIdx.x, lane = tid & 31;
+  grid_dep_wait();
+  grid_dep_launch();
+  for (int i = tid; i < kBins; i += blockDim.x) bins[i] = 0;
+  if (tid == 0) top_s = 1;
+  __syncthreads();
+  // a sequence is walked by one warp, a block by one lane
+  auto each = [&](auto &&f) {
+    for (int b = tid >> 5; b < a.batch; b += blockDim.x >> 5) {
+      int q0, lq, k0, lk;
+      if (!seq_range(a, b, q0, lq, k0, lk)) {
+        if (lane == 0) set_error(a.err, kErrRange);
+        continue;
+      }
+      for (int r = lane * a.tile; r < lq; r += 32 * a.tile) {
+        PromptItem it{};
+        it.q0 = q0 + r;
+        it.rows = min(a.tile, lq - r);
+        it.k0 = k0;
+        it.lk = lk;
+        it.see = r + lk - lq + 1;
+        f(it, max(0, min(lk, it.see + it.rows - 1)));
+      }
+    }
+  };
+  int top = 1;
+  for (int b = tid; b < a.batch; b += blockDim.x) {
+    int q0, lq, k0, lk;
+    if (seq_range(a, b, q0, lq, k0, lk) && lq > 0) top = max(top, lk);
+  }
+  atomicMax(&top_s, top);
+  __syncthreads();
+  top = top_s;
+  auto bin_of = [&](int keys) { return kBins - 1 - (int)((long)keys * (kBins - 1) / top); };
+  each([&](const PromptItem &, int keys) { atomicAdd(&bins[bin_of(keys)], 1); });
+  __syncthreads();
+  // exclusive scan of the bins (one a thread)
+  const int n = bins[tid];
+  int v = n;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int w = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += w;
+  }
+  if (lane == 31) warp_tot[tid >> 5] = v;
+  __syncthreads();
+  if (tid < 32) {
+    int w = warp_tot[tid];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, w, o);
+      if (tid >= o) w += z;
+    }
+    warp_tot[tid] = w;
+  }
+  __syncthreads();
+  const int incl = v + ((tid >> 5) ? warp_tot[(tid >> 5) - 1] : 0);
+  bins[tid] = incl - n;
+  if (tid == kBins - 1) {
+    a.hdr->items = incl;
+    a.hdr->next = 0;
+  }
+  __syncthreads();
+  each([&](const PromptItem &it, int keys) { a.items[atomicAdd(&bins[bin_of(keys)], 1)] = it; });
+}
+
+// ---------------------------------------------------------------------------
+// fp32 attention over packed sequences (validation path)
+// ---------------------------------------------------------------------------
+
+constexpr int kSimtKeys = 32;
+
+// One block of 16 rows of one head per CTA (128 threads), 32 keys at a time
+// through shared memory, one pass with the running maximum and sum.
+template <class T>
+__global__ void __launch_bounds__(128) prompt_attn_simt(PromptAttnArgs a) {
+  extern __shared__ float sm[];
+  const int dq = a.d_nope + a.d_rope, ldk = dq + 1;
+  float *qs = sm;                           // [16][dq]
+  float *ks = qs + kPromptTileSimt * dq;    // [32][dq + 1]
+  float *vs = ks + kSimtKeys * ldk;         // [32][d_v]
+  float *ps = vs + kSimtKeys * a.d_v;       // [16][33]
+  __shared__ float m_s[kPromptTileSimt], l_s[kPromptTileSimt], f_s[kPromptTileSimt];
+  grid_dep_wait();
+  if ((int)blockIdx.x >= a.hdr->items) return;
+  const PromptItem it = a.items[blockIdx.x];
+  const int h = blockIdx.y, kv = h / (a.n_heads / a.n_kv_heads), tid = threadIdx.x;
+  const T *qn = static_cast<const T *>(a.q_nope.ptr) + h * a.q_nope.head;
+  const T *qr = static_cast<const T *>(a.q_rope.ptr) + h * a.q_rope.head;
+  const T *kn = static_cast<const T *>(a.k_nope.ptr) + kv * a.k_nope.head;
+  const T *kr = static_cast<const T *>(a.k_rope);
+  const T *vp = static_cast<const T *>(a.v.ptr) + kv * a.v.head;
+  for (int i = tid; i < it.rows * dq; i += blockDim.x) {
+    const int r = i / dq, c = i % dq;
+    const long t = it.q0 + r;
+    qs[i] = c < a.d_nope ? ld_f(qn + t * a.q_nope.token + c)
+                         : ld_f(qr + t * a.q_rope.token + c - a.d_nope);
+  }
+  if (tid < kPromptTileSimt) {
+    m_s[tid] = -INFINITY;
+    l_s[tid] = 0.f;
+  }
+  const int cols = (a.d_v + 7) / 8;  // a thread: row tid / 8, values tid % 8 + 8 j
+  float acc[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) acc[j] = 0.f;
+  const int r_o = tid >> 3, c_o = tid & 7;
+  const int keys = max(0, min(it.lk, it.see + it.rows - 1));
+  for (int j0 = 0; j0 < keys; j0 += kSimtKeys) {
+    const int nk = min(kSimtKeys, keys - j0);
+    __syncthreads();
+    for (int i = tid; i < nk * dq; i += blockDim.x) {
+      const int j = i / dq, c = i % dq;
+      const long t = it.k0 + j0 + j;
+      ks[j * ldk + c] = c < a.d_nope ? ld_f(kn + t * a.k_nope.token + c)
+                                     : ld_f(kr + t * a.k_rope_stride + c - a.d_nope);
+    }
+    for (int i = tid; i < nk * a.d_v; i += blockDim.x) {
+      const int j = i / a.d_v, c = i % a.d_v;
+      vs[i] = ld_f(vp + (it.k0 + j0 + j) * a.v.token + c);
+    }
+    __syncthreads();
+    // scores: warp w has rows w, w + 4, ...; lane = key
+    for (int r = tid >> 5; r < kPromptTileSimt; r += 4) {
+      const int j = tid & 31;
+      const bool seen = r < it.rows && j < nk && j0 + j < it.see + r;
+      float x = 0.f;
+      if (seen)
+        for (int c = 0; c < dq; ++c) x = fmaf(qs[r * dq + c], ks[j * ldk + c], x);
+      x = seen ? x * a.scale : -INFINITY;
+      const float m0 = m_s[r], m1 = fmaxf(m0, warp_max(x));
+      const float base = m1 == -INFINITY ? 0.f : m1;
+      const float p = seen ? expf(x - base) : 0.f;
+      const float sum = warp_sum(p);
+      ps[r * 33 + j] = p;
+      if (j == 0) {
+        const float f = expf(m0 - base);
+        f_s[r] = f;
+        l_s[r] = l_s[r] * f + sum;
+        m_s[r] = m1;
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+    // a row adds up only the keys it sees: a masked value is never multiplied
+    const float f = f_s[r_o];
+    const int mine = max(0, min(nk, it.see + r_o - j0));
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j >= cols) break;
+      const int c = c_o + 8 * j;
+      if (c >= a.d_v) continue;
+      float o = acc[j] * f;
+      for (int k = 0; k < mine; ++k) o = fmaf(ps[r_o * 33 + k], vs[k * a.d_v + c], o);
+      acc[j] = o;
+    }
+  }
+  __syncthreads();
+  if (r_o >= it.rows) return;
+  const float l = l_s[r_o], inv = l == 0.f ? 0.f : 1.f / l;
+  const long at = (long)(it.q0 + r_o) * a.n_heads + h;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const int c = c_o + 8 * j;
+    if (j < cols && c < a.d_v) static_cast<T *>(a.out)[at * a.d_v + c] = st_cast<T>(acc[j] * inv);
+  }
+  if (a.lse && c_o == 0) a.lse[at] = l == 0.f ? -INFINITY : m_s[r_o] + logf(l);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_append_f32(const PromptAppendArgs &a, const RopeParams &rp,
+                                     cudaStream_t s) {
+  return launch_pdl(prompt_append_f32, dim3(a.n_tokens), dim3(128), 0, s, a, rp);
+}
+
+cudaError_t launch_prompt_append_bf16(const PromptAppendArgs &a, const RopeParams &rp,
+                                      bool int8_rows, cudaStream_t s) {
+  int group = 1;  // warps a token
+  if (a.q.ptr) {
+    const int slabs = (a.n_heads + kSlab - 1) / kSlab;
+    group += slabs < 8 ? slabs : 8;
+  }
+  const int per = group >= 8 ? 1 : 8 / group;
+  const dim3 grid((a.n_tokens + per - 1) / per), block(32 * per * group);
+  return int8_rows ? launch_pdl(prompt_append_bf16<true>, grid, block, 0, s, a, rp, group)
+                   : launch_pdl(prompt_append_bf16<false>, grid, block, 0, s, a, rp, group);
+}
+
+cudaError_t launch_gather_f32(const GatherArgs &a, int row, cudaStream_t s) {
+  return launch_pdl(gather_f32, dim3((a.n_rows + 7) / 8), dim3(256), 0, s, a, row);
+}
+
+cudaError_t launch_gather_bf16(const GatherArgs &a, bool int8_rows, cudaStream_t s) {
+  const dim3 grid((a.n_rows + 7) / 8);
+  return int8_rows ? launch_pdl(gather_bf16<true>, grid, dim3(256), 0, s, a)
+                   : launch_pdl(gather_bf16<false>, grid, dim3(256), 0, s, a);
+}
+
+cudaError_t launch_prompt_plan(const PromptPlanArgs &a, cudaStream_t s) {
+  static_assert(kBins == 1024, "the scan takes one bin a thread");
+  return launch_pdl(prompt_plan_kernel, dim3(1), dim3(kBins), 0, s, a);
+}
+
+template <class T>
+cudaError_t launch_prompt_attn_simt(const PromptAttnArgs &a, cudaStream_t s) {
+  const int dq = a.d_nope + a.d_rope;
+  const size_t smem = sizeof(float) * (kPromptTileSimt * dq + kSimtKeys * (dq + 1) +
+                                       kSimtKeys * a.d_v + kPromptTileSimt * 33);
+  static api::PerDeviceOnce once;
+  const cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(prompt_attn_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                120 * 1024);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prompt_attn_simt<T>, dim3((unsigned)a.max_items, a.n_heads), dim3(128), smem, s,
+                    a);
+}
+template cudaError_t launch_prompt_attn_simt<float>(const PromptAttnArgs &, cudaStream_t);
+template cudaError_t launch_prompt_attn_simt<bf16>(const PromptAttnArgs &, cudaStream_t);
+
+}  // namespace mla

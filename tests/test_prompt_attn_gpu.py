@@ -1,0 +1,247 @@
+"""Causal attention over packed sequences against its formula in 64 bits."""
+
+import math
+
+import pytest
+import torch
+
+from mla_latent_kv_45_b200 import _lib as L
+from mla_latent_kv_45_b200 import build
+from prompt_testlib import (TINY, V2, attn_inputs, check_attn, dims_of, i32, offsets, run_attn,
+                            workspace)
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build.build()
+    L.lib()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+def go(dims, new, total, kv, seed=1, spread=1.0):
+    cu_q, cu_k = offsets(new), offsets(total)
+    t = attn_inputs(dims, cu_q[-1], cu_k[-1], kv, seed, spread)
+    out, lse = run_attn(dims, t, cu_q, cu_k)
+    check_attn(dims, t, cu_q, cu_k, out, lse)
+    return t, out, lse
+
+
+@pytest.mark.parametrize("n", [1, 2, 16, 17, 63, 64, 65, 115, 127, 128, 129, 200, 255, 256, 257,
+                               383, 385, 511, 513, 1000])
+def test_one_prompt(n):
+    go(dims_of(V2, 2, BF), [n], [n], 2, seed=n)
+
+
+@pytest.mark.parametrize("n,m", [(1, 1), (1, 64), (1, 127), (1, 128), (1, 129), (1, 5000), (3, 130),
+                                 (64, 4097), (128, 1000), (129, 385), (256, 4352), (300, 301),
+                                 (257, 2500)])
+def test_chunk_behind_cached_rows(n, m):
+    go(dims_of(V2, 3, BF), [n], [m], 3, seed=n + m)
+
+
+@pytest.mark.parametrize("heads,kv", [(1, 1), (4, 1), (4, 2), (6, 2), (6, 3), (5, 5), (128, 128),
+                                      (128, 8), (256, 1)])
+def test_head_layouts(heads, kv):
+    go(dims_of(V2, heads, BF), [70, 1, 190], [70, 150, 200], kv, seed=heads)
+
+
+def test_packed_lengths_of_every_kind():
+    new = [0, 1, 128, 0, 129, 5, 700, 64, 256, 0]
+    total = [0, 1, 128, 40, 129, 300, 700, 1000, 257, 0]
+    go(dims_of(V2, 4, BF), new, total, 4)
+
+
+def test_many_sequences():
+    new = [(7 * i) % 40 for i in range(400)]
+    total = [n + (11 * i) % 90 for i, n in enumerate(new)]
+    go(dims_of(V2, 2, BF), new, total, 1)
+
+
+def test_queries_that_see_no_key():
+    """lq > lk: the first lq - lk queries see nothing and get zeros and -inf."""
+    new, total = [200, 5, 130, 300], [72, 0, 1, 20]
+    go(dims_of(V2, 2, BF), new, total, 2)
+
+
+def test_no_keys_at_all():
+    dims = dims_of(V2, 2, BF)
+    t = attn_inputs(dims, 150, 0, 2, 3)
+    out, lse = run_attn(dims, t, [0, 100, 150], [0, 0, 0])
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+def test_no_queries():
+    dims = dims_of(V2, 2, BF)
+    t = attn_inputs(dims, 0, 50, 2, 3)
+    out, lse = run_attn(dims, t, [0, 0], [0, 50])
+    assert out.numel() == 0
+
+
+@pytest.mark.parametrize("spread", [3.0, 8.0])
+def test_wide_scores(spread):
+    """Scores far apart: the running maximum moves by more than a rescale threshold."""
+    go(dims_of(V2, 2, BF), [400, 333], [400, 900], 2, spread=spread)
+
+
+def test_rising_scores_rescale():
+    """Every later key outweighs all earlier ones: each tile lifts the maximum."""
+    dims = dims_of(V2, 2, BF)
+    n = 900
+    t = attn_inputs(dims, n, n, 2, 5)
+    ramp = torch.linspace(0, 40, n, device="cuda")
+    t["q_nope"] = torch.ones_like(t["q_nope"])
+    t["k_nope"] = (ramp[:, None, None] / 10 + 0.1 * t["k_nope"].float()).to(BF)
+    out, lse = run_attn(dims, t, [0, n], [0, n])
+    check_attn(dims, t, [0, n], [0, n], out, lse)
+
+
+def test_scale_of_the_caller():
+    go(dims_of(V2, 2, BF, scale=0.5), [200], [300], 2)
+
+
+def test_views_of_wider_tensors():
+    """Queries and keys as slices of [tokens, heads, 192] and [tokens, heads, 256] products,
+    and tensors stored head by head."""
+    dims = dims_of(V2, 3, BF)
+    new, total = [150, 90], [150, 333]
+    cu_q, cu_k = offsets(new), offsets(total)
+    t = attn_inputs(dims, cu_q[-1], cu_k[-1], 3, 9)
+    ref_out, ref_lse = run_attn(dims, t, cu_q, cu_k)
+    q = torch.cat([t["q_nope"], t["q_rope"]], -1)
+    kv = torch.cat([t["k_nope"], t["v"]], -1)
+    rows = torch.cat([torch.zeros(cu_k[-1], 512, dtype=BF, device="cuda"), t["k_rope"]], -1)
+    s = dict(q_nope=q[..., :128], q_rope=q[..., 128:], k_nope=kv[..., :128], v=kv[..., 128:],
+             k_rope=rows[:, 512:])
+    out, lse = run_attn(dims, s, cu_q, cu_k)
+    assert torch.equal(out, ref_out) and torch.equal(lse, ref_lse)
+    s = {k: (x.transpose(0, 1).contiguous().transpose(0, 1) if x.dim() == 3 else x)
+         for k, x in t.items()}
+    out, lse = run_attn(dims, s, cu_q, cu_k)
+    assert torch.equal(out, ref_out) and torch.equal(lse, ref_lse)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_what_lies_outside_the_sequences(dtype):
+    """NaN and infinities in front of the first sequence, behind the last one and in the next
+    sequence's keys reach nothing; rows outside the sequences keep what they held."""
+    dims = dims_of(V2, 2, dtype)
+    cu_q, cu_k = [5, 75, 205], [9, 109, 259]
+    t = attn_inputs(dims, 260, 300, 2, 11)
+    for name in ("q_nope", "q_rope"):
+        t[name][:5] = math.nan
+        t[name][205:] = math.inf
+    for name in ("k_nope", "k_rope", "v"):
+        t[name][:9] = math.nan
+        t[name][259:] = -math.inf
+    clean = {k: v.clone() for k, v in t.items()}
+    out, lse = run_attn(dims, t, cu_q, cu_k)
+    check_attn(dims, t, cu_q, cu_k, out, lse)
+    for lo, hi in ((0, 5), (205, 260)):
+        assert (out[lo:hi] == 7).all() and (lse[lo:hi] == 7).all()
+    for name in ("k_nope", "k_rope", "v"):   # the second sequence's keys turn bad: the first's rows stay
+        t[name][109:259] = math.nan
+    out2, lse2 = run_attn(dims, t, cu_q, cu_k)
+    assert torch.equal(out2[:75], out[:75]) and torch.equal(lse2[:75], lse[:75])
+    for name in clean:
+        assert clean[name].shape == t[name].shape
+
+
+def test_later_keys_of_a_sequence_reach_no_earlier_row():
+    """Keys that a row does not see may hold anything, values anything finite."""
+    dims = dims_of(V2, 2, BF)
+    n = 300
+    t = attn_inputs(dims, n, n, 2, 13)
+    out, lse = run_attn(dims, t, [0, n], [0, n])
+    t["k_nope"][200:] = math.nan
+    t["v"][200:] = torch.finfo(BF).max
+    out2, lse2 = run_attn(dims, t, [0, n], [0, n])
+    assert torch.equal(out2[:200], out[:200]) and torch.equal(lse2[:200], lse[:200])
+
+
+@pytest.mark.parametrize("size,heads,kv", [(TINY, 4, 4), (TINY, 6, 2), (V2, 2, 1),
+                                           (dict(d_c=64, d_rope=2, d_nope=5, d_v=3), 3, 3),
+                                           (dict(d_c=64, d_rope=128, d_nope=256, d_v=256), 2, 2)])
+def test_fp32(size, heads, kv):
+    go(dims_of(size, heads, F32), [33, 0, 1, 70, 16], [33, 4, 50, 81, 10], kv)
+
+
+def test_without_lse():
+    dims = dims_of(V2, 2, BF)
+    t = attn_inputs(dims, 140, 140, 2, 15)
+    want, _ = run_attn(dims, t, [0, 140], [0, 140])
+    ws = workspace(dims, 1, 140)
+    out = torch.empty_like(want)
+    L.mla_prompt_attn(dims, t["q_nope"], t["q_rope"], t["k_nope"], t["k_rope"], t["v"],
+                      i32([0, 140]), i32([0, 140]), out, None, ws)
+    assert torch.equal(out, want)
+
+
+def test_bad_offsets_skip_their_sequence():
+    """Descending offsets or offsets outside the tensors: the sequence's rows keep what they
+    held, the others are computed and the error word is set."""
+    dims = dims_of(V2, 2, BF)
+    t = attn_inputs(dims, 300, 300, 2, 17)
+    ws = workspace(dims, 3, 300)
+    for cu_q, cu_k, bad in (([0, 100, 90, 300], [0, 100, 100, 300], slice(90, 90)),
+                            ([0, 100, 200, 301], [0, 100, 200, 300], slice(200, 300)),
+                            ([0, 100, 200, 300], [0, 100, 200, 400], slice(200, 300)),
+                            ([0, 100, 200, 300], [-4, 100, 200, 300], slice(0, 100))):
+        out = torch.full((300, 2, 128), 7.0, dtype=BF, device="cuda")
+        lse = torch.full((300, 2), 7.0, device="cuda")
+        L.mla_prompt_attn(dims, t["q_nope"], t["q_rope"], t["k_nope"], t["k_rope"], t["v"],
+                          i32(cu_q), i32(cu_k), out, lse, ws)
+        assert L.mla_get_device_error(ws) == 6
+        assert (out[bad] == 7).all() and (lse[bad] == 7).all()
+        assert L.mla_get_device_error(ws) == 0
+    run_attn(dims, t, [0, 100, 200, 300], [0, 100, 200, 300], ws=ws)
+
+
+def test_same_bits_every_time_and_on_other_streams():
+    dims = dims_of(V2, 8, BF)
+    new = [300, 17, 513, 128]
+    cu = offsets(new)
+    t = attn_inputs(dims, cu[-1], cu[-1], 8, 19)
+    out, lse = run_attn(dims, t, cu, cu)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    cud = i32(cu)
+    bufs = [(workspace(dims, 4, cu[-1]), torch.empty_like(out), torch.empty_like(lse))
+            for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, (ws, o, e) in zip((s1, s2), bufs):
+            L.mla_prompt_attn(dims, t["q_nope"], t["q_rope"], t["k_nope"], t["k_rope"], t["v"], cud,
+                              cud, o, e, ws, s)
+            got.append((o, e))
+    torch.cuda.synchronize()
+    for o, e in got:
+        assert torch.equal(o, out) and torch.equal(e, lse)
+
+
+def test_captured_and_replayed_with_other_lengths():
+    """A graph reads the offsets at replay: other lengths within the captured sizes."""
+    dims = dims_of(V2, 4, BF)
+    t = attn_inputs(dims, 400, 600, 4, 21)
+    cu_q, cu_k = i32([0, 400, 400]), i32([0, 600, 600])
+    ws = workspace(dims, 2, 400)
+    out = torch.empty(400, 4, 128, dtype=BF, device="cuda")
+    lse = torch.empty(400, 4, device="cuda")
+    call = lambda s=None: L.mla_prompt_attn(dims, t["q_nope"], t["q_rope"], t["k_nope"],  # noqa: E731
+                                            t["k_rope"], t["v"], cu_q, cu_k, out, lse, ws, s)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for q, k in (([0, 400, 400], [0, 600, 600]), ([0, 130, 400], [0, 130, 500]),
+                 ([0, 1, 300], [0, 40, 600])):
+        cu_q.copy_(i32(q))
+        cu_k.copy_(i32(k))
+        g.replay()
+        torch.cuda.synchronize()
+        assert L.mla_get_device_error(ws) == 0
+        check_attn(dims, t, q, k, out, lse, str(q))
