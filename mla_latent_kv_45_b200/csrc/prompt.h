@@ -91,8 +91,14 @@ struct PromptAttnArgs {
 };
 
 constexpr int kPromptTileSimt = 16;
+constexpr int kPromptTileSm100 = 256;
 
 template <class T>
 cudaError_t launch_prompt_attn_simt(const PromptAttnArgs &a, cudaStream_t s);
+
+namespace sm100 {
+// bf16, d_nope = d_v = 128, d_rope = 64, items of at most kPromptTileSm100 rows
+cudaError_t launch_prompt_attn(const PromptAttnArgs &a, cudaStream_t s);
+}  // namespace sm100
 
 }  // namespace mla

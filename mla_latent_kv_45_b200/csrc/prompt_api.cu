@@ -22,8 +22,7 @@ using api::aligned4;
 mla_status cuda_ok(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
 
 int tile_rows(const mla_dims &d) {
-  (void)d;
-  return kPromptTileSimt;
+  return d.dtype == MLA_BF16 ? kPromptTileSm100 : kPromptTileSimt;
 }
 
 // The error word and the plan header share the first 256 bytes (the part that
@@ -205,7 +204,7 @@ mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, in
   a.lse = lse;
   a.err = pa.err;
   if (d.dtype == MLA_FP32) return cuda_ok(launch_prompt_attn_simt<float>(a, s));
-  return cuda_ok(launch_prompt_attn_simt<__nv_bfloat16>(a, s));
+  return cuda_ok(sm100::launch_prompt_attn(a, s));
 }
 
 }  // extern "C"

@@ -592,6 +592,5 @@ cudaError_t launch_prompt_attn_simt(const PromptAttnArgs &a, cudaStream_t s) {
                     a);
 }
 template cudaError_t launch_prompt_attn_simt<float>(const PromptAttnArgs &, cudaStream_t);
-template cudaError_t launch_prompt_attn_simt<bf16>(const PromptAttnArgs &, cudaStream_t);
 
 }  // namespace mla
