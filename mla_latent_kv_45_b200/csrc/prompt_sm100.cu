@@ -88,7 +88,7 @@ __device__ __forceinline__ bool wait_bar(const Ctx &c, uint64_t *bar, uint32_t p
   if (mbar_try_wait(a, parity)) return true;
   const uint64_t t0 = globaltimer();
   while (true) {
-    if (mbar_try_wait_sleep(a, parity, kSleepNs)) return true;
+    if (mbar_try_wait(a, parity)) return true;
     if (c.bars->abort) return false;
     if (globaltimer() - t0 > kTimeoutNs) {
       set_error(c.err, kErrTimeout);
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = (c0 + c) % kSlots;
           if (!wait(&bars->full[s], ((c0 + c) / kSlots) & 1)) return false;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             const uint64_t qd = qd0 + (uint64_t)(((3 * t + c) * kChunk) >> 4);
             const uint64_t kd = kd0 + (uint64_t)((s * kChunk) >> 4);
   #pragma unroll
@@ -415,12 +415,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         kd + (uint64_t)((32 * k) >> 4), kIdescS, (c | k) ? 1u : 0u);
           }
         }
-        if (lane == 0) umma_commit(&bars->s_full[t]);
+        if (elect_one()) umma_commit(&bars->s_full[t]);
         __syncwarp();
         return true;
       };
       auto release = [&](int c0, int n) {
-        if (lane == 0)
+        if (elect_one())
           for (int c = 0; c < n; ++c) umma_commit(&bars->empty[(c0 + c) % kSlots]);
         __syncwarp();
       };
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&bars->p_full[t], np[t] & 1)) return false;
         ++np[t];
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
   #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const uint64_t vd = vd0 + (uint64_t)((((c0 + c) % kSlots) * kChunk) >> 4);
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&bars->q_full[t], nq[t] & 1)) return false;
         ++nq[t];
         if (!scores(t, nl)) return false;
-        if (n_t[t] == 1 && lane == 0) umma_commit(&bars->q_empty[t]);
+        if (n_t[t] == 1 && elect_one()) umma_commit(&bars->q_empty[t]);
         __syncwarp();
         return true;
       };
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if (!last && j + 1 < nt[t]) {
               ok = scores(t, k0);
-              if (ok && j + 2 == nt[t] && lane == 0) umma_commit(&bars->q_empty[t]);
+              if (ok && j + 2 == nt[t] && elect_one()) umma_commit(&bars->q_empty[t]);
               __syncwarp();
             } else if (last && more) {
               ok = first_scores(t);
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           nl = last && !more ? k0 : k0 + 3;
         }
       }
-      if (lane == 0) {
+      if (elect_one()) {
         umma_commit(&bars->drain);
         drain_bar(&bars->drain, 0);
       }

@@ -49,6 +49,19 @@ __device__ __forceinline__ uint32_t mapa(uint32_t saddr, uint32_t rank) {
   return r;
 }
 
+// True in one lane of a converged warp (the same one every time).  Unlike a
+// comparison of the lane number this tells the compiler that a single thread
+// remains, so that the operands of tcgen05 instructions need no uniformity loop.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Moves a warpgroup's registers per thread to N (every warp of it executes this).
 template <int N>
 __device__ __forceinline__ void regs_raise() {
