@@ -39,7 +39,7 @@ constexpr int kTile = 128;              // rows of a tile, keys of a step
 constexpr int kChunk = 16384;           // bytes of a ring slot and of a 64-column box of Q
 constexpr int kSlots = 8;
 constexpr int kSched = 3;               // work items in flight between the warps
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarps = 12;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpFix = 10, kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
 // Registers a thread: a softmax row keeps its 128 scores, the third warpgroup (two
 // of its warps idle) needs few.  Launched with 65536 / 384 = 168 (a multiple of 8).
@@ -47,6 +47,15 @@ constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kSleepNs = 20000;
+
+// Of every kPolyOf pairs of weights kPolyPairs are exponentiated on the FMA pipe
+// and the rest on the special-function unit.
+constexpr int kPolyOf = 8, kPolyPairs = 3;
+constexpr float kExpC0 = 0.999999285f;
+constexpr float kExpC1 = 0.693121791f;
+constexpr float kExpC2 = 0.240247443f;
+constexpr float kExpC3 = 0.0559178889f;
+constexpr float kExpC4 = 0.00957011059f;
 
 constexpr int kOffQ = 0;                          // [2 tiles][3 boxes]
 constexpr int kOffRing = kOffQ + 6 * kChunk;
@@ -64,12 +73,17 @@ struct Work {
   int head;   // -1: no more work
 };
 
+// Steps are counted through (g) over all items of a CTA.  Step g's keys are ring
+// chunks 5 g .. 5 g + 2 (mod 8), its values 5 g + 3 and 5 g + 4, so the keys of g take the
+// place of the last key chunk and the values of g - 2, the values of g that of the
+// first two key chunks of g - 1.
 struct Bars {
-  uint64_t full[kSlots], empty[kSlots];
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2];   // of step g at g % 2
+  uint64_t v_raw[2];      // values that end inside the step landed; the fixing warp fills v_full
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2];     // scores of the tile complete
-  uint64_t p_full[2];     // P written (and O rescaled) by the tile's four warps
-  uint64_t pv_done[2];    // O += P V complete
+  uint64_t s_full[2];     // scores of the tile complete (and its P V products so far)
+  uint64_t p_full[2][2];  // half of P written (and O rescaled) by the tile's four warps
+  uint64_t o_full[2];     // the item's last O += P V complete
   uint64_t w_full[kSched], w_empty[kSched];
   uint64_t drain;
   Work work[kSched];
@@ -111,6 +125,37 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+__device__ __forceinline__ uint64_t exp2_sfu(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return f2_pack(ex2(a), ex2(b));
+}
+
+// 2^x of two values x <= 8 on the FMA pipe: x = i + f with i the nearest integer
+// (x + 1.5 2^23 holds it in its low bits), 2^f by a polynomial of degree 4 that
+// is the minimax fit of the relative error on [-1/2, 1/2] (2.6e-6), 2^i by adding i
+// to the exponent.  Below -126 (a masked score is -inf) the result is zero, as the
+// special-function unit's is.
+__device__ __forceinline__ uint64_t exp2_poly(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  const uint64_t big = f2_pack(12582912.f, 12582912.f), neg = f2_pack(-12582912.f, -12582912.f);
+  const uint64_t r = f2_add(x, big);
+  const uint64_t i = f2_add(r, neg);
+  const uint64_t f = f2_fma(i, f2_pack(-1.f, -1.f), x);
+  uint64_t p = f2_pack(kExpC4, kExpC4);
+  p = f2_fma(p, f, f2_pack(kExpC3, kExpC3));
+  p = f2_fma(p, f, f2_pack(kExpC2, kExpC2));
+  p = f2_fma(p, f, f2_pack(kExpC1, kExpC1));
+  p = f2_fma(p, f, f2_pack(kExpC0, kExpC0));
+  float r0, r1, p0, p1;
+  f2_unpack(r, r0, r1);
+  f2_unpack(p, p0, p1);
+  p0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(r0) << 23));
+  p1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(r1) << 23));
+  return f2_pack(a < -126.f ? 0.f : p0, b < -126.f ? 0.f : p1);
+}
+
 // Rows of tile t of an item, and the steps of 128 keys that its last row sees.
 __device__ __forceinline__ int tile_rows(const PromptItem &it, int t) {
   return max(0, min(kTile, it.rows - t * kTile));
@@ -137,20 +182,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&bars->full[i], 1);
-      mbar_init(&bars->empty[i], 1);
-    }
     for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->k_full[t], 1);
+      mbar_init(&bars->k_free[t], 1);
+      mbar_init(&bars->v_full[t], 1);
+      mbar_init(&bars->v_free[t], 1);
+      mbar_init(&bars->v_raw[t], 1);
       mbar_init(&bars->q_full[t], 1);
       mbar_init(&bars->q_empty[t], 1);
       mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->p_full[t], 4);
-      mbar_init(&bars->pv_done[t], 1);
+      mbar_init(&bars->p_full[t][0], 4);
+      mbar_init(&bars->p_full[t][1], 4);
+      mbar_init(&bars->o_full[t], 1);
     }
     for (int i = 0; i < kSched; ++i) {
       mbar_init(&bars->w_full[i], 1);
-      mbar_init(&bars->w_empty[i], 9);   // the MMA warp and the eight softmax warps
+      mbar_init(&bars->w_empty[i], 10);   // the MMA and the fixing warp, eight softmax warps
     }
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
@@ -196,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem + lane_off + kTmemS + 128 * t;
     const uint32_t o_addr = tmem + lane_off + kTmemO + 128 * t;
-    int ns = 0;      // steps of this tile so far
+    int ns = 0, no = 0;      // steps and items of this tile so far
     bool ok = true;
     Work w;
     for (int k = 0; ok && take(k, w); ++k) {
@@ -221,21 +268,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-        for (int c = 4; c < 128; c += 8) {
+        for (int c = 4; c < 124; c += 8) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mx[i] = fmaxf(mx[i], c + 4 + i < 128 ? fmaxf(v[c + i], v[c + 4 + i]) : v[c + i]);
+          for (int i = 0; i < 4; ++i) mx[i] = max3_nan(mx[i], v[c + i], v[c + 4 + i]);
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
-        const float m_new = top > m + 8.0f || m == -INFINITY ? top : m;
+        mx[0] = max3_nan(mx[0], v[124], v[125]);
+        mx[1] = max3_nan(mx[1], v[126], v[127]);
+        const float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale_log2;
+        // NaN (a NaN score that the row sees) takes over m, and with it l and O
+        const float m_new = top <= m + 8.0f && m != -INFINITY ? m : top;
         const bool moved = m_new != m;
         const float base = m_new == -INFINITY ? 0.f : m_new;   // a row that sees nothing so far
         if (j > 0 && __any_sync(0xffffffffu, moved)) {
           const float f = moved ? ex2(m - base) : 1.f;
           l *= f;
-          ok = __all_sync(0xffffffffu, wait_bar(ctx, &bars->pv_done[t], (ns - 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 128; c += 16) {
             uint32_t r[16];
@@ -247,30 +293,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         m = m_new;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t sum[2] = {0, 0};
+        const uint64_t scale2 = f2_pack(scale_log2, scale_log2), base2 = f2_pack(-base, -base);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t p[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float a0 = ex2(fmaf(v[64 * h + 2 * i], scale_log2, -base));
-            const float a1 = ex2(fmaf(v[64 * h + 2 * i + 1], scale_log2, -base));
-            sum[(2 * i) & 3] += a0;
-            sum[(2 * i + 1) & 3] += a1;
-            p[i] = pack2(a0, a1);
+            const uint64_t x = f2_fma(f2_pack(v[64 * h + 2 * i], v[64 * h + 2 * i + 1]), scale2, base2);
+            const uint64_t e = i % kPolyOf < kPolyPairs ? exp2_poly(x) : exp2_sfu(x);
+            sum[i & 1] = f2_add(sum[i & 1], e);
+            float e0, e1;
+            f2_unpack(e, e0, e1);
+            p[i] = pack2(e0, e1);
           }
           tmem_st32(s_addr + 32 * h, p);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_full[t][h]);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[t]);
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float s0, s1;
+        f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
       }
       if (!ok) break;
       // ---- the item's rows
       if (steps > 0) {
-        ok = __all_sync(0xffffffffu, wait_bar(ctx, &bars->pv_done[t], (ns - 1) & 1));
+        ok = __all_sync(0xffffffffu, wait_bar(ctx, &bars->o_full[t], no++ & 1));
         if (!ok) break;
         tc_fence_after();
       }
@@ -306,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rep = a.n_heads / a.n_kv_heads;
         const int items = a.hdr->items, total = items * a.n_heads;
         const int group_work = items * heads_per_group;
-        int nl = 0, nq[2] = {0, 0};
+        int gk = 0, gv = 0, nq[2] = {0, 0}, raw[2] = {0, 0};
+        bool tail[2] = {false, false};
         bool ok = true;
         int idx = blockIdx.x;
         for (int k = 0; ok; ++k) {
@@ -329,34 +380,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             n_t[t] = tile_steps(w.it, t);
             n = max(n, n_t[t]);
           }
-          auto slot_for = [&]() -> int {
-            const int s = nl % kSlots;
-            if (nl >= kSlots && !wait_bar(ctx, &bars->empty[s], ((nl / kSlots) - 1) & 1)) return -1;
-            ++nl;
-            mbar_expect_tx(&bars->full[s], kChunk);
-            return s;
-          };
+          auto ring = [&](int c) { return smem + kOffRing + (c & (kSlots - 1)) * kChunk; };
           auto load_k = [&](int j) -> bool {
+            const int g = gk, u = g & 1;
+            if (g >= 2 && (!wait_bar(ctx, &bars->k_free[u], ((g >> 1) - 1) & 1) ||
+                           !wait_bar(ctx, &bars->v_free[u], ((g >> 1) - 1) & 1)))
+              return false;
+            ++gk;
             const int tok = w.it.k0 + j * kTile;
-            for (int c = 0; c < 3; ++c) {
-              const int s = slot_for();
-              if (s < 0) return false;
-              uint8_t *dst = smem + kOffRing + s * kChunk;
-              if (c < 2)
-                tma_load_3d(dst, &tm_kn, 64 * c, kv, tok, &bars->full[s]);
-              else
-                tma_load_2d(dst, &tm_kr, 0, tok, &bars->full[s]);
-            }
+            mbar_expect_tx(&bars->k_full[u], 3 * kChunk);
+            tma_load_3d(ring(5 * g), &tm_kn, 0, kv, tok, &bars->k_full[u]);
+            tma_load_3d(ring(5 * g + 1), &tm_kn, 64, kv, tok, &bars->k_full[u]);
+            tma_load_2d(ring(5 * g + 2), &tm_kr, 0, tok, &bars->k_full[u]);
             return true;
           };
           auto load_v = [&](int j) -> bool {
+            const int g = gv, u = g & 1;
+            if (g >= 1 && !wait_bar(ctx, &bars->k_free[u ^ 1], ((g - 1) >> 1) & 1)) return false;
+            ++gv;
+            tail[u] = w.it.lk - j * kTile < kTile;
+            raw[u] += tail[u];
+            uint64_t *bar = tail[u] ? &bars->v_raw[u] : &bars->v_full[u];
+            mbar_expect_tx(bar, 2 * kChunk);
             for (int c = 0; c < 2; ++c) {
-              const int s = slot_for();
-              if (s < 0) return false;
-              uint8_t *dst = smem + kOffRing + s * kChunk;
+              uint8_t *dst = ring(5 * g + 3 + c);
               const int tok = w.it.k0 + j * kTile + 64 * c;
-              tma_load_3d(dst, &tm_v, 0, kv, tok, &bars->full[s]);
-              tma_load_3d(dst + kChunk / 2, &tm_v, 64, kv, tok, &bars->full[s]);
+              tma_load_3d(dst, &tm_v, 0, kv, tok, bar);
+              tma_load_3d(dst + kChunk / 2, &tm_v, 64, kv, tok, bar);
             }
             return true;
           };
@@ -383,150 +433,148 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (bars->abort) {
           // what is in flight must land before the CTA ends
-          for (int i = max(0, nl - kSlots); i < nl; ++i)
-            drain_bar(&bars->full[i % kSlots], (i / kSlots) & 1);
+          for (int g = max(0, gk - 2); g < gk; ++g) drain_bar(&bars->k_full[g & 1], (g >> 1) & 1);
+          for (int g = max(0, gv - 2); g < gv; ++g)
+            if (tail[g & 1])
+              drain_bar(&bars->v_raw[g & 1], (raw[g & 1] - 1) & 1);
+            else
+              drain_bar(&bars->v_full[g & 1], (g >> 1) & 1);
           for (int t = 0; t < 2; ++t)
             if (nq[t] > 0) drain_bar(&bars->q_full[t], (nq[t] - 1) & 1);
         }
       }
+    } else if (warp == kWarpFix) {
+      // Rows behind a sequence's last key belong to another sequence and may hold
+      // anything: 0 * NaN must not reach O, so the values there are zeroed.
+      int g0 = 0;
+      uint32_t ph[2] = {0, 0};
+      Work w;
+      for (int k = 0; take(k, w); ++k) {
+        const int n = max(tile_steps(w.it, 0), tile_steps(w.it, 1));
+        const int left = w.it.lk - (n - 1) * kTile;   // keys of the item's last step
+        if (n > 0 && left < kTile) {
+          const int g = g0 + n - 1, u = g & 1;
+          if (!__all_sync(0xffffffffu, wait_bar(ctx, &bars->v_raw[u], u ? ph[1] : ph[0]))) break;
+          ph[0] ^= u ^ 1;
+          ph[1] ^= u;
+          for (int i = left * 16 + lane; i < kTile * 16; i += 32) {
+            const int row = i >> 4, c = 5 * g + 3 + (row >> 6);
+            *reinterpret_cast<uint4 *>(smem + kOffRing + (c & (kSlots - 1)) * kChunk +
+                                       ((i >> 3) & 1) * (kChunk / 2) + (row & 63) * 128 +
+                                       (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->v_full[u]);
+        }
+        g0 += n;
+      }
     } else if (warp == kWarpMma) {
-      const uint64_t qd0 = sdesc(smem_u32(smem + kOffQ), 16, 1024, 2);
-      const uint64_t kd0 = sdesc(smem_u32(smem + kOffRing), 16, 1024, 2);
-      const uint64_t vd0 = sdesc(smem_u32(smem + kOffRing), kChunk / 2, 1024, 2);
-      int nl = 0;               // ring chunks consumed (and released)
-      int np[2] = {0, 0};       // P tiles consumed
-      int nq[2] = {0, 0};       // Q tiles consumed
-      auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        const bool ok = wait_bar(ctx, bar, parity);
-        return __all_sync(0xffffffffu, ok);
-      };
-      // S of tile t from the three ring chunks that start at chunk c0
-      auto scores = [&](int t, int c0) -> bool {
-        for (int c = 0; c < 3; ++c) {
-          const int s = (c0 + c) % kSlots;
-          if (!wait(&bars->full[s], ((c0 + c) / kSlots) & 1)) return false;
-          tc_fence_after();
-          if (elect_one()) {
+      if (elect_one()) {
+        const uint64_t qd0 = sdesc(smem_u32(smem + kOffQ), 16, 1024, 2);
+        const uint64_t kd0 = sdesc(smem_u32(smem + kOffRing), 16, 1024, 2);
+        const uint64_t vd0 = sdesc(smem_u32(smem + kOffRing), kChunk / 2, 1024, 2);
+        int g = 0, ni = 0;   // steps and items so far
+        uint32_t p_ph[2] = {0, 0}, q_ph[2] = {0, 0};
+        Work w;
+        int n_t[2] = {0, 0}, n = 0;
+        // the next item that has any keys
+        auto next_work = [&]() -> bool {
+          while (true) {
+            const int slot = ni % kSched;
+            if (!wait_bar(ctx, &bars->w_full[slot], (ni / kSched) & 1)) return false;
+            ++ni;
+            w = bars->work[slot];
+            mbar_arrive(&bars->w_empty[slot]);
+            if (w.head < 0) return false;
+            n_t[0] = tile_steps(w.it, 0);
+            n_t[1] = tile_steps(w.it, 1);
+            n = max(n_t[0], n_t[1]);
+            if (n > 0) return true;
+          }
+        };
+        // S of tile t = Q K^T with the keys of step gk
+        auto scores = [&](int t, int gk) {
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
             const uint64_t qd = qd0 + (uint64_t)(((3 * t + c) * kChunk) >> 4);
-            const uint64_t kd = kd0 + (uint64_t)((s * kChunk) >> 4);
-  #pragma unroll
+            const uint64_t kd = kd0 + (uint64_t)((((5 * gk + c) & (kSlots - 1)) * kChunk) >> 4);
+#pragma unroll
             for (int k = 0; k < 4; ++k)
               umma_bf16(tmem + kTmemS + 128 * t, qd + (uint64_t)((32 * k) >> 4),
                         kd + (uint64_t)((32 * k) >> 4), kIdescS, (c | k) ? 1u : 0u);
           }
+          umma_commit(&bars->s_full[t]);
+        };
+        auto k_ready = [&](int gk) {
+          const bool r = wait_bar(ctx, &bars->k_full[gk & 1], (gk >> 1) & 1);
+          tc_fence_after();
+          return r;
+        };
+        // S of step 0 of the current item's tile t
+        auto first_scores = [&](int t, int gk) -> bool {
+          if (!wait_bar(ctx, &bars->q_full[t], q_ph[t])) return false;
+          q_ph[t] ^= 1;
+          tc_fence_after();
+          scores(t, gk);
+          if (n_t[t] == 1) umma_commit(&bars->q_empty[t]);
+          return true;
+        };
+        bool more = next_work(), ok = true;
+        if (more) {
+          ok = k_ready(0);
+          for (int t = 0; t < 2 && ok; ++t)
+            if (n_t[t] > 0) ok = first_scores(t, 0);
+          if (ok) umma_commit(&bars->k_free[0]);
         }
-        if (elect_one()) umma_commit(&bars->s_full[t]);
-        __syncwarp();
-        return true;
-      };
-      auto release = [&](int c0, int n) {
-        if (elect_one())
-          for (int c = 0; c < n; ++c) umma_commit(&bars->empty[(c0 + c) % kSlots]);
-        __syncwarp();
-      };
-      // O of tile t += P V, V in the two chunks that start at c0; `left` keys of the step exist
-      auto values = [&](int t, int c0, int left, bool zero, bool first) -> bool {
-        for (int c = 0; c < 2; ++c) {
-          const int s = (c0 + c) % kSlots;
-          if (!wait(&bars->full[s], ((c0 + c) / kSlots) & 1)) return false;
-          if (zero && left < 64 * (c + 1)) {
-            // rows behind the sequence's last key belong to another sequence and
-            // may hold anything: 0 * NaN must not reach O
-            uint8_t *v = smem + kOffRing + s * kChunk;
-            const int from = max(0, left - 64 * c);
-            for (int i = lane; i < (64 - from) * 16; i += 32) {
-              const int row = from + (i >> 4);
-              *reinterpret_cast<uint4 *>(v + ((i >> 3) & 1) * (kChunk / 2) + row * 128 +
-                                         (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+        while (more && ok) {
+          const int steps = n, nt[2] = {n_t[0], n_t[1]};
+          for (int j = 0; j < steps && ok; ++j, ++g) {
+            const bool last = j + 1 == steps;
+            if (last) more = next_work();
+            const bool keys = !last || more;    // step g + 1 exists
+            ok = wait_bar(ctx, &bars->v_full[g & 1], (g >> 1) & 1);
+            bool keys_in = false;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (ok && j < nt[t]) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  ok = ok && wait_bar(ctx, &bars->p_full[t][h], p_ph[t]);
+                  if (!ok) break;
+                  tc_fence_after();
+                  const uint64_t vd =
+                      vd0 + (uint64_t)((((5 * g + 3 + h) & (kSlots - 1)) * kChunk) >> 4);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    umma_bf16_ts(tmem + kTmemO + 128 * t, tmem + kTmemS + 128 * t + 32 * h + 8 * k,
+                                 vd + (uint64_t)((2048 * k) >> 4), kIdescPV,
+                                 (j == 0 && h == 0 && k == 0) ? 0u : 1u);
+                }
+                p_ph[t] ^= 1;
+                if (j + 1 == nt[t]) umma_commit(&bars->o_full[t]);
+              }
+              if (!ok) break;
+              if (t == 1) umma_commit(&bars->v_free[g & 1]);
+              if (last ? more && n_t[t] > 0 : j + 1 < nt[t]) {
+                if (!keys_in) ok = k_ready(g + 1);
+                keys_in = true;
+                if (!ok) break;
+                if (last) {
+                  ok = first_scores(t, g + 1);
+                } else {
+                  scores(t, g + 1);
+                  if (j + 2 == nt[t]) umma_commit(&bars->q_empty[t]);
+                }
+              }
+              if (!ok) break;
             }
-            fence_proxy_async_smem();
-            __syncwarp();
+            if (ok && keys) umma_commit(&bars->k_free[(g + 1) & 1]);
           }
         }
-        if (!wait(&bars->p_full[t], np[t] & 1)) return false;
-        ++np[t];
-        tc_fence_after();
-        if (elect_one()) {
-  #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint64_t vd = vd0 + (uint64_t)((((c0 + c) % kSlots) * kChunk) >> 4);
-  #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_bf16_ts(tmem + kTmemO + 128 * t, tmem + kTmemS + 128 * t + 32 * c + 8 * k,
-                           vd + (uint64_t)((2048 * k) >> 4), kIdescPV,
-                           (first && c == 0 && k == 0) ? 0u : 1u);
-          }
-          umma_commit(&bars->pv_done[t]);
-        }
-        __syncwarp();
-        return true;
-      };
-      int k = 0;
-      int n_t[2] = {0, 0}, n = 0;
-      Work w;
-      // the next item that has any keys
-      auto next_work = [&]() -> bool {
-        while (take(k, w)) {
-          ++k;
-          n_t[0] = tile_steps(w.it, 0);
-          n_t[1] = tile_steps(w.it, 1);
-          n = max(n_t[0], n_t[1]);
-          if (n > 0) return true;
-        }
-        return false;
-      };
-      // S of step 0 of the item's tile t
-      auto first_scores = [&](int t) -> bool {
-        if (n_t[t] == 0) return true;
-        if (!wait(&bars->q_full[t], nq[t] & 1)) return false;
-        ++nq[t];
-        if (!scores(t, nl)) return false;
-        if (n_t[t] == 1 && elect_one()) umma_commit(&bars->q_empty[t]);
-        __syncwarp();
-        return true;
-      };
-      bool more = next_work();
-      bool ok = true;
-      if (more) {
-        ok = first_scores(0) && first_scores(1);
-        if (ok) release(nl, 3);
-        nl += 3;
-      }
-      while (more && ok) {
-        const Work cur = w;
-        const int steps = n, nt[2] = {n_t[0], n_t[1]};
-        for (int j = 0; j < steps && ok; ++j) {
-          const int v0 = nl, k0 = nl + 2;
-          const bool last = j + 1 == steps;
-          const int left = cur.it.lk - j * kTile;
-          if (last) more = next_work();
-          bool zero = left < kTile;
-          if (last) nl = k0;      // first_scores reads the next item's keys there
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (j < nt[t]) {
-              ok = values(t, v0, left, zero, j == 0);
-              zero = false;
-            }
-            if (!ok) break;
-            if (!last && j + 1 < nt[t]) {
-              ok = scores(t, k0);
-              if (ok && j + 2 == nt[t] && elect_one()) umma_commit(&bars->q_empty[t]);
-              __syncwarp();
-            } else if (last && more) {
-              ok = first_scores(t);
-            }
-          }
-          if (!ok) break;
-          release(v0, 2);
-          if (!last || more) release(k0, 3);
-          nl = last && !more ? k0 : k0 + 3;
-        }
-      }
-      if (elect_one()) {
         umma_commit(&bars->drain);
         drain_bar(&bars->drain, 0);
       }
-      __syncwarp();
     }
   }
 
