@@ -48,15 +48,6 @@ static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kSleepNs = 20000;
 
-// Of every kPolyOf pairs of weights kPolyPairs are exponentiated on the FMA pipe
-// and the rest on the special-function unit.
-constexpr int kPolyOf = 8, kPolyPairs = 3;
-constexpr float kExpC0 = 0.999999285f;
-constexpr float kExpC1 = 0.693121791f;
-constexpr float kExpC2 = 0.240247443f;
-constexpr float kExpC3 = 0.0559178889f;
-constexpr float kExpC4 = 0.00957011059f;
-
 constexpr int kOffQ = 0;                          // [2 tiles][3 boxes]
 constexpr int kOffRing = kOffQ + 6 * kChunk;
 constexpr int kOffBar = kOffRing + kSlots * kChunk;
@@ -129,31 +120,6 @@ __device__ __forceinline__ uint64_t exp2_sfu(uint64_t x) {
   float a, b;
   f2_unpack(x, a, b);
   return f2_pack(ex2(a), ex2(b));
-}
-
-// 2^x of two values x <= 8 on the FMA pipe: x = i + f with i the nearest integer
-// (x + 1.5 2^23 holds it in its low bits), 2^f by a polynomial of degree 4 that
-// is the minimax fit of the relative error on [-1/2, 1/2] (2.6e-6), 2^i by adding i
-// to the exponent.  Below -126 (a masked score is -inf) the result is zero, as the
-// special-function unit's is.
-__device__ __forceinline__ uint64_t exp2_poly(uint64_t x) {
-  float a, b;
-  f2_unpack(x, a, b);
-  const uint64_t big = f2_pack(12582912.f, 12582912.f), neg = f2_pack(-12582912.f, -12582912.f);
-  const uint64_t r = f2_add(x, big);
-  const uint64_t i = f2_add(r, neg);
-  const uint64_t f = f2_fma(i, f2_pack(-1.f, -1.f), x);
-  uint64_t p = f2_pack(kExpC4, kExpC4);
-  p = f2_fma(p, f, f2_pack(kExpC3, kExpC3));
-  p = f2_fma(p, f, f2_pack(kExpC2, kExpC2));
-  p = f2_fma(p, f, f2_pack(kExpC1, kExpC1));
-  p = f2_fma(p, f, f2_pack(kExpC0, kExpC0));
-  float r0, r1, p0, p1;
-  f2_unpack(r, r0, r1);
-  f2_unpack(p, p0, p1);
-  p0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(r0) << 23));
-  p1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(r1) << 23));
-  return f2_pack(a < -126.f ? 0.f : p0, b < -126.f ? 0.f : p1);
 }
 
 // Rows of tile t of an item, and the steps of 128 keys that its last row sees.
@@ -301,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const uint64_t x = f2_fma(f2_pack(v[64 * h + 2 * i], v[64 * h + 2 * i + 1]), scale2, base2);
-            const uint64_t e = i % kPolyOf < kPolyPairs ? exp2_poly(x) : exp2_sfu(x);
+            const uint64_t e = exp2_sfu(x);
             sum[i & 1] = f2_add(sum[i & 1], e);
             float e0, e1;
             f2_unpack(e, e0, e1);
