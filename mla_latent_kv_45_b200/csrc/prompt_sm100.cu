@@ -39,19 +39,21 @@ constexpr int kTile = 128;              // rows of a tile, keys of a step
 constexpr int kChunk = 16384;           // bytes of a ring slot and of a 64-column box of Q
 constexpr int kSlots = 8;
 constexpr int kSched = 3;               // work items in flight between the warps
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpFix = 10, kWarps = 12;
+constexpr int kWarpOut = 8;             // warps 8-11 write the output
+constexpr int kWarpLoad = 12, kWarpMma = 13, kWarpFix = 14, kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-// Registers a thread: a softmax row keeps its 128 scores, the third warpgroup (two
-// of its warps idle) needs few.  Launched with 65536 / 384 = 168 (a multiple of 8).
-constexpr int kRegsSoftmax = 200, kRegsOther = 104;
-static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
+// Registers a thread: a softmax row keeps its 128 scores, the other two
+// warpgroups (one warp idle) need few.  Launched with 65536 / 512 = 128.
+constexpr int kRegsSoftmax = 176, kRegsOther = 80;
+static_assert(256 * kRegsSoftmax + 256 * kRegsOther <= kThreads * 128, "register split");
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kSleepNs = 20000;
 
 constexpr int kOffQ = 0;                          // [2 tiles][3 boxes]
 constexpr int kOffRing = kOffQ + 6 * kChunk;
 constexpr int kOffBar = kOffRing + kSlots * kChunk;
-constexpr int kSmemBytes = kOffBar + 1024 + 1024;
+constexpr int kOffInv = kOffBar + 1024;           // [2 tiles][128] 1 / row sum
+constexpr int kSmemBytes = kOffInv + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;   // tile t at + 128 t
@@ -75,6 +77,8 @@ struct Bars {
   uint64_t s_full[2];     // scores of the tile complete (and its P V products so far)
   uint64_t p_full[2][2];  // half of P written (and O rescaled) by the tile's four warps
   uint64_t o_full[2];     // the item's last O += P V complete
+  uint64_t l_full[2];     // the reciprocal row sums are in shared memory
+  uint64_t o_free[2];     // O and the row sums have been read
   uint64_t w_full[kSched], w_empty[kSched];
   uint64_t drain;
   Work work[kSched];
@@ -122,6 +126,15 @@ __device__ __forceinline__ uint64_t exp2_sfu(uint64_t x) {
   return f2_pack(ex2(a), ex2(b));
 }
 
+// 32 bytes (a whole sector of L2) to a 32-byte aligned address.
+__device__ __forceinline__ void st_global_32(void *p, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d, uint32_t e, uint32_t f, uint32_t g,
+                                             uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b),
+               "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+               : "memory");
+}
+
 // Rows of tile t of an item, and the steps of 128 keys that its last row sees.
 __device__ __forceinline__ int tile_rows(const PromptItem &it, int t) {
   return max(0, min(kTile, it.rows - t * kTile));
@@ -140,13 +153,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tm_kr,
                        const __grid_constant__ CUtensorMap tm_v, const PromptAttnArgs a,
                        const float scale_log2, const int heads_per_group) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw;
   Bars *bars = reinterpret_cast<Bars *>(smem + kOffBar);
   const Ctx ctx{bars, a.err};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  // The swizzled boxes need a 1024-byte boundary, which the dynamic shared memory
+  // starts on (there is no static part in front of it).
+  if (smem_u32(smem) & 1023) {
+    if (threadIdx.x == 0) set_error(a.err, kErrTimeout);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->k_full[t], 1);
@@ -160,10 +178,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->p_full[t][0], 4);
       mbar_init(&bars->p_full[t][1], 4);
       mbar_init(&bars->o_full[t], 1);
+      mbar_init(&bars->l_full[t], 4);
+      mbar_init(&bars->o_free[t], 4);
     }
     for (int i = 0; i < kSched; ++i) {
       mbar_init(&bars->w_full[i], 1);
-      mbar_init(&bars->w_empty[i], 10);   // the MMA and the fixing warp, eight softmax warps
+      mbar_init(&bars->w_empty[i], 14);   // eight softmax, four output warps, MMA, fixing
     }
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
@@ -209,13 +229,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem + lane_off + kTmemS + 128 * t;
     const uint32_t o_addr = tmem + lane_off + kTmemO + 128 * t;
-    int ns = 0, no = 0;      // steps and items of this tile so far
+    float *inv_s = reinterpret_cast<float *>(smem + kOffInv) + 128 * t;
+    int ns = 0, ni = 0;      // steps and items (with keys) of this tile so far
     bool ok = true;
     Work w;
     for (int k = 0; ok && take(k, w); ++k) {
       const int rows = tile_rows(w.it, t);
-      if (rows == 0) continue;
       const int steps = tile_steps(w.it, t);
+      if (steps == 0) continue;
       const int see = max(0, min(w.it.lk, w.it.see + t * kTile + row));   // keys this row sees
       const int see_warp = __shfl_sync(0xffffffffu, see, 0);              // ... the warp's fewest
       float m = -INFINITY, l = 0.f;
@@ -263,17 +284,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t scale2 = f2_pack(scale_log2, scale_log2), base2 = f2_pack(-base, -base);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t p[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const uint64_t x = f2_fma(f2_pack(v[64 * h + 2 * i], v[64 * h + 2 * i + 1]), scale2, base2);
-            const uint64_t e = exp2_sfu(x);
-            sum[i & 1] = f2_add(sum[i & 1], e);
-            float e0, e1;
-            f2_unpack(e, e0, e1);
-            p[i] = pack2(e0, e1);
+          for (int q = 0; q < 2; ++q) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int c = 64 * h + 32 * q + 2 * i;
+              const uint64_t e = exp2_sfu(f2_fma(f2_pack(v[c], v[c + 1]), scale2, base2));
+              sum[i & 1] = f2_add(sum[i & 1], e);
+              float e0, e1;
+              f2_unpack(e, e0, e1);
+              p[i] = pack2(e0, e1);
+            }
+            tmem_st16(s_addr + 32 * h + 16 * q, p);
           }
-          tmem_st32(s_addr + 32 * h, p);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -284,40 +308,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += s0 + s1;
       }
       if (!ok) break;
-      // ---- the item's rows
-      if (steps > 0) {
-        ok = __all_sync(0xffffffffu, wait_bar(ctx, &bars->o_full[t], no++ & 1));
-        if (!ok) break;
-        tc_fence_after();
-      }
-      const float inv = see > 0 ? 1.f / l : 0.f;
-      const long at = (long)(w.it.q0 + t * kTile + row) * a.n_heads + w.head;
+      // ---- the item's row sums, for the output warps
+      if (ni > 0)
+        ok = __all_sync(0xffffffffu, wait_bar(ctx, &bars->o_free[t], (ni - 1) & 1));
+      if (!ok) break;
+      ++ni;
+      inv_s[row] = 1.f / l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->l_full[t]);
       if (row < rows && a.lse)
-        a.lse[at] = see > 0 ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
-      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<bf16 *>(a.out) + at * 128);
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        float o[32];
-        if (steps > 0) {
-          tmem_ld32f(o_addr + 32 * c, o);
-          tmem_wait_ld();
-        }
-        if (row < rows) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[e] = see > 0 ? pack2(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv) : 0u;
-            dst[4 * c + i] = make_uint4(x[0], x[1], x[2], x[3]);
-          }
-        }
-      }
-      tc_fence_before();   // O is free: the next P of this tile says so to the MMA warp
+        a.lse[(long)(w.it.q0 + t * kTile + row) * a.n_heads + w.head] =
+            see > 0 ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
   } else {
     regs_lower<kRegsOther>();
-    if (warp == kWarpLoad) {
+    if (warp < kWarpOut + 4) {
+      // ---------- output: O / row sum of the tile's rows, one thread a row, while the
+      // softmax warps go on with the next item
+      const int row = (warp & 3) * 32 + lane;
+      const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const float *inv_s = reinterpret_cast<const float *>(smem + kOffInv);
+      int no[2] = {0, 0};
+      bool ok = true;
+      Work w;
+      for (int k = 0; ok && take(k, w); ++k) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int rows = tile_rows(w.it, t), steps = tile_steps(w.it, t);
+          if (rows == 0) continue;
+          const int see = min(w.it.lk, w.it.see + t * kTile + row);
+          const long at = (long)(w.it.q0 + t * kTile + row) * a.n_heads + w.head;
+          bf16 *dst = static_cast<bf16 *>(a.out) + at * 128;
+          if (steps == 0) {      // no row of the tile sees a key
+            if (row < rows) {
+              for (int c = 0; c < 128; c += 16) st_global_32(dst + c, 0, 0, 0, 0, 0, 0, 0, 0);
+              if (a.lse) a.lse[at] = -INFINITY;
+            }
+            continue;
+          }
+          ok = wait_bar(ctx, &bars->l_full[t], no[t] & 1) &&
+               wait_bar(ctx, &bars->o_full[t], no[t] & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          ++no[t];
+          tc_fence_after();
+          const float inv = inv_s[128 * t + row];
+          const uint32_t o_addr = tmem + lane_off + kTmemO + 128 * t;
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            float o[32];
+            tmem_ld32f(o_addr + c, o);
+            tmem_wait_ld();
+            if (c == 96) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars->o_free[t]);
+            }
+            uint32_t x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              x[i] = see > 0 ? pack2(o[2 * i] * inv, o[2 * i + 1] * inv) : 0u;
+            if (row < rows) {
+              st_global_32(dst + c, x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
+              st_global_32(dst + c + 16, x[8], x[9], x[10], x[11], x[12], x[13], x[14], x[15]);
+            }
+          }
+        }
+      }
+    } else if (warp == kWarpLoad) {
       if (lane == 0) {
         const int rep = a.n_heads / a.n_kv_heads;
         const int items = a.hdr->items, total = items * a.n_heads;
@@ -441,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t kd0 = sdesc(smem_u32(smem + kOffRing), 16, 1024, 2);
         const uint64_t vd0 = sdesc(smem_u32(smem + kOffRing), kChunk / 2, 1024, 2);
         int g = 0, ni = 0;   // steps and items so far
+        int no[2] = {0, 0};          // items with keys, per tile
         uint32_t p_ph[2] = {0, 0}, q_ph[2] = {0, 0};
         Work w;
         int n_t[2] = {0, 0}, n = 0;
@@ -504,6 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (ok && j < nt[t]) {
+                // the first product of an item overwrites the O of the one before
+                if (j == 0 && no[t]++ > 0) ok = wait_bar(ctx, &bars->o_free[t], (no[t] - 2) & 1);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   ok = ok && wait_bar(ctx, &bars->p_full[t][h], p_ph[t]);
