@@ -295,8 +295,7 @@ mla_status mla_cache_gather(const mla_dims *dims, const mla_paged_cache *cache, 
  * q_nope: [n_q][n_heads][d_nope]; q_rope: [n_q][n_heads][d_rope], rotated;
  * k_nope: [n_k][n_kv_heads][d_nope]; v: [n_k][n_kv_heads][d_v]; k_rope:
  * [n_k][d_rope], rotated, rows k_rope_stride elements apart; out:
- * [n_q][n_heads][d_v] (with MLA_BF16 32-byte aligned); lse: [n_q][n_heads] fp32
- * or NULL.  k_nope, k_rope and v
+ * [n_q][n_heads][d_v]; lse: [n_q][n_heads] fp32 or NULL.  k_nope, k_rope and v
  * may be NULL when n_k is 0.  With MLA_BF16 the weights of a softmax are rounded
  * to bf16 for the product with v (their sum is not); scores, maxima, sums and
  * the accumulator are fp32.  Keys and values outside their own sequence never

@@ -159,8 +159,7 @@ mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, in
   MLA_TRY(check_ws(ws, ws_bytes, prompt_ws_bytes(d, batch, n_q)));
   if (n_q == 0) return MLA_OK;
   if (!out) return MLA_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(out) & (d.dtype == MLA_BF16 ? 31 : 15))
-    return MLA_ERR_ALIGNMENT;
+  if (!aligned16(out)) return MLA_ERR_ALIGNMENT;
   MLA_TRY(check_heads(d, q_nope, n_q, d.n_heads, d.d_nope));
   MLA_TRY(check_heads(d, q_rope, n_q, d.n_heads, d.d_rope));
   if (n_k > 0) {

@@ -99,7 +99,7 @@ def test_attn_refusals(lib):
                 dict(qn=heads(None)), dict(kn=heads(A, 0, 128)), dict(v=heads(A, 16384, 127)),
                 dict(qr=heads(A, 63, 64)), dict(krs=63), dict(krs=-64)):
         assert attn(lib, **bad) == ARG, bad
-    for bad in (dict(cu_q=A + 2), dict(cu_k=A + 1), dict(out=A + 8), dict(out=A + 16), dict(lse=A + 2),
+    for bad in (dict(cu_q=A + 2), dict(cu_k=A + 1), dict(out=A + 8), dict(lse=A + 2),
                 dict(qn=heads(A + 8, 16384, 128)), dict(kr=A + 4), dict(krs=68), dict(ws=A + 8),
                 dict(kn=heads(A, 16388, 128)), dict(v=heads(A, 16384, 132))):
         assert attn(lib, **bad) == ALIGN, bad
