@@ -445,6 +445,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kv = w.head / rep;
         const int n_t[2] = {tile_steps(w.it, 0), tile_steps(w.it, 1)};
         const int n = max(n_t[0], n_t[1]);
+        // Q of tile t, once the item before has its last scores
+        auto load_q = [&](int t) -> bool {
+          if (n_t[t] == 0) return true;
+          if (nq[t] > 0 && !wait_bar(ctx, &bars->q_empty[t], (nq[t] - 1) & 1)) return false;
+          ++nq[t];
+          uint8_t *q = smem + kOffQ + t * kQTile;
+          const int row = w.it.q0 + t * kRows;
+          mbar_expect_tx(&bars->q_full[t], kQTile);
+          tma_load_3d(q, &tm_qn, 0, w.head, row, &bars->q_full[t]);
+          tma_load_3d(q + kQBox, &tm_qn, 64, w.head, row, &bars->q_full[t]);
+          tma_load_3d(q + 2 * kQBox, &tm_qr, 0, w.head, row, &bars->q_full[t]);
+          return true;
+        };
+        // tile 0 is through with its Q first: it sees fewer keys
+        if (n > 0) ok = load_q(0);
         for (int j = 0; j < n && ok; ++j) {
           const int g = gk, u = g & 1, tok = w.it.k0 + j * kKeys;
           if (g >= 2 && !wait_bar(ctx, &bars->k_free[u], ((g >> 1) - 1) & 1)) {
@@ -461,20 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           v_tok = tok;
           v_kv = kv;
           v_left = w.it.lk - j * kKeys;
-          for (int t = 0; j == 0 && t < 2 && ok; ++t) {
-            if (n_t[t] == 0) continue;
-            if (nq[t] > 0 && !wait_bar(ctx, &bars->q_empty[t], (nq[t] - 1) & 1)) {
-              ok = false;
-              break;
-            }
-            ++nq[t];
-            uint8_t *q = smem + kOffQ + t * kQTile;
-            const int row = w.it.q0 + t * kRows;
-            mbar_expect_tx(&bars->q_full[t], kQTile);
-            tma_load_3d(q, &tm_qn, 0, w.head, row, &bars->q_full[t]);
-            tma_load_3d(q + kQBox, &tm_qn, 64, w.head, row, &bars->q_full[t]);
-            tma_load_3d(q + 2 * kQBox, &tm_qr, 0, w.head, row, &bars->q_full[t]);
-          }
+          if (j == 0 && ok) ok = load_q(1);
         }
       }
       if (ok && !bars->abort && gv < gk) load_v();
