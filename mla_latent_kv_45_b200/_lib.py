@@ -77,7 +77,9 @@ class Dims:
     cache_format: int = MLA_CACHE_NATIVE
 
     def c(self) -> _Dims:
-        return _Dims(*dataclasses.astuple(self))
+        return _Dims(self.n_heads, self.d_c, self.d_rope, self.d_nope, self.d_v, self.page_size,
+                     self.dtype, self.rope_layout, self.rope_base, self.rms_eps,
+                     self.softmax_scale, self.cache_format)
 
     @property
     def torch_dtype(self):
@@ -232,64 +234,79 @@ def mla_unabsorb_out(dims: Dims, z, W_UV, W_O, out, ws: torch.Tensor, stream=Non
         ws.numel() * ws.element_size(), _stream(stream)))
 
 
-def _heads(fn: str, dims: Dims, t: torch.Tensor, name: str, heads: int, width: int) -> _Heads:
+# The checks below stand between a small call and its launch, so each looks at a
+# tensor's attributes once.
+
+def _bad(fn: str, name: str, t: torch.Tensor, want) -> ValueError:
+    return ValueError(f"{fn}: {name} is {t.dtype} {tuple(t.shape)} with strides {t.stride()} on "
+                      f"{t.device}; wanted {want}")
+
+
+def _heads(fn: str, dtype, dev: int, t: torch.Tensor, name: str, tokens: int, heads: int,
+           width: int) -> _Heads:
     """The view of a [tokens, heads, width] tensor (any token and head strides)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != width:
-        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not [tokens, {heads}, {width}]")
-    _typed(fn, dims, t, name)
-    return _Heads(t.data_ptr(), t.stride(0), t.stride(1))
+    st = t.stride()
+    if (t.dtype is not dtype or t.shape != (tokens, heads, width) or st[2] != 1 and width > 1
+            or t.get_device() != dev):
+        raise _bad(fn, name, t, f"{dtype} [{tokens}, {heads}, {width}] on cuda:{dev}, last axis "
+                                "contiguous")
+    return _Heads(t.data_ptr(), st[0], st[1])
 
 
-def _typed(fn: str, dims: Dims, t: torch.Tensor, name: str, last: bool = True):
-    if t.dtype != dims.torch_dtype:
-        raise ValueError(f"{fn}: {name} is {t.dtype}, not {dims.torch_dtype}")
-    if last and t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{fn}: the last axis of {name} is not contiguous")
+def _rows(fn: str, dtype, dev: int, t: torch.Tensor, name: str, rows: int, width: int):
+    """Address and row stride of a [rows, width] tensor (any row stride)."""
+    st = t.stride()
+    if (t.dtype is not dtype or t.shape != (rows, width) or st[1] != 1 and width > 1
+            or t.get_device() != dev):
+        raise _bad(fn, name, t, f"{dtype} [{rows}, {width}] on cuda:{dev}, last axis contiguous")
+    return t.data_ptr(), st[0]
 
 
-def _offsets(fn: str, t: Optional[torch.Tensor], name: str, n: Optional[int] = None):
-    if t is None:
-        return
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} is not a contiguous int32 vector")
-    if n is not None and t.numel() != n:
-        raise ValueError(f"{fn}: {name} has {t.numel()} entries, not {n}")
+def _dense(fn: str, dtype, dev: int, t: torch.Tensor, name: str, shape) -> int:
+    """Address of a contiguous tensor of this type and shape."""
+    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != dev):
+        raise _bad(fn, name, t, f"{dtype} {tuple(shape)} on cuda:{dev}, contiguous")
+    return t.data_ptr()
 
 
-def _same_device(fn: str, *tensors):
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1 or next(iter(devs)).type != "cuda":
-        raise ValueError(f"{fn}: tensors on {sorted(map(str, devs))}, not on one CUDA device")
-    return next(iter(devs))
+def _device(fn: str, t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{fn}: tensors on {t.device}, not on a CUDA device")
+    return dev
 
 
-def _on(dev, stream):
-    """The stream to launch on (default: the device's current one), checked against the device."""
-    if stream is None:
-        return torch.cuda.current_stream(dev)
-    if stream.device != dev:
-        raise ValueError(f"stream on {stream.device}, tensors on {dev}")
-    return stream
-
-
-def _contiguous(fn: str, t: Optional[torch.Tensor], name: str, shape, dtype):
-    if t is None:
-        return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} is {t.dtype} {tuple(t.shape)}, not a contiguous "
-                         f"{dtype} {tuple(shape)}")
-
-
-def _paged(fn: str, dims: Dims, cache: PagedCache, batch: int):
+def _paged(fn: str, dims: Dims, dev: int, cache: PagedCache, batch: int) -> _Cache:
     if dims.cache_format == MLA_CACHE_INT8:
         width, dtype = MLA_INT8_ROW_BYTES, torch.uint8
     else:
         width, dtype = dims.d_c + dims.d_rope, dims.torch_dtype
-    _contiguous(fn, cache.pool, "pool", (cache.pool.shape[0], dims.page_size, width), dtype)
-    if cache.block_table.dim() != 2 or cache.block_table.shape[0] != batch:
-        raise ValueError(f"{fn}: block_table has shape {tuple(cache.block_table.shape)}, "
-                         f"not [{batch}, max_pages]")
-    _contiguous(fn, cache.block_table, "block_table", cache.block_table.shape, torch.int32)
+    pages, table = cache.pool.shape[0], cache.block_table.shape[-1]
+    return _Cache(_dense(fn, dtype, dev, cache.pool, "pool", (pages, dims.page_size, width)), pages,
+                  _dense(fn, torch.int32, dev, cache.block_table, "block_table", (batch, table)),
+                  table, None if cache.seq_lens is None else cache.seq_lens.data_ptr())
+
+
+def _launch(fn: str, call, dev: int, ws: torch.Tensor, stream, *args):
+    """Calls the library on `stream` (default: the tensors' device's current one), with the
+    tensors' device current."""
+    if ws is None or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"{fn}: ws is not a contiguous tensor on cuda:{dev}")
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"{fn}: stream on {stream.device}, tensors on cuda:{dev}")
+    here = torch.cuda.current_device()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    try:
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        st = call(*args, ws.data_ptr(), ws.nbytes, stream.cuda_stream)
+    finally:
+        if here != dev:
+            torch.cuda.set_device(here)
+    if st != 0:
+        raise MlaError(fn, st)
 
 
 def mla_prompt_workspace_size(dims: Dims, batch: int, n_tokens: int) -> int:
@@ -305,49 +322,34 @@ def mla_prompt_append(dims: Dims, cache: PagedCache, x, gamma, cu_tokens, ctx_le
     ctx_lens ``[batch]`` int32 or None, q_rope and q_out ``[tokens, n_heads,
     d_rope]`` (any token and head strides; q_out may be q_rope) or None.
     """
-    fn = "mla_prompt_append"
-    _offsets(fn, cu_tokens, "cu_tokens")
-    batch = cu_tokens.numel() - 1
-    _offsets(fn, ctx_lens, "ctx_lens", batch)
-    _paged(fn, dims, cache, batch)
-    if x.dim() != 2 or x.shape[1] != dims.d_c + dims.d_rope:
-        raise ValueError(f"{fn}: x has shape {tuple(x.shape)}, not [tokens, {dims.d_c + dims.d_rope}]")
-    _typed(fn, dims, x, "x")
-    _contiguous(fn, gamma, "gamma", (dims.d_c,), dims.torch_dtype)
+    fn, dt, i32 = "mla_prompt_append", dims.torch_dtype, torch.int32
+    dev, n, batch = _device(fn, x), x.shape[0], cu_tokens.numel() - 1
+    xp, xs = _rows(fn, dt, dev, x, "x", n, dims.d_c + dims.d_rope)
     if (q_rope is None) != (q_out is None):
         raise ValueError(f"{fn}: q_rope and q_out go together")
-    dev = _same_device(fn, x, gamma, cu_tokens, ctx_lens, cache.pool, cache.block_table, q_rope,
-                       q_out, ws)
     q = qo = None
     if q_rope is not None:
-        if q_rope.shape[0] != x.shape[0] or q_out.shape[0] != x.shape[0]:
-            raise ValueError(f"{fn}: x, q_rope and q_out differ in their number of tokens")
-        q = ctypes.byref(_heads(fn, dims, q_rope, "q_rope", dims.n_heads, dims.d_rope))
-        qo = ctypes.byref(_heads(fn, dims, q_out, "q_out", dims.n_heads, dims.d_rope))
-    d, c = dims.c(), cache.c()
-    with torch.cuda.device(dev):
-        _ok(fn, lib().mla_prompt_append(
-            ctypes.byref(d), ctypes.byref(c), batch, x.shape[0], _p(x), x.stride(0), _p(gamma),
-            _p(cu_tokens), _p(ctx_lens), q, qo, _p(ws), ws.numel() * ws.element_size(),
-            _stream(_on(dev, stream))))
+        q = ctypes.byref(_heads(fn, dt, dev, q_rope, "q_rope", n, dims.n_heads, dims.d_rope))
+        qo = ctypes.byref(_heads(fn, dt, dev, q_out, "q_out", n, dims.n_heads, dims.d_rope))
+    _launch(fn, lib().mla_prompt_append, dev, ws, stream, ctypes.byref(dims.c()),
+            ctypes.byref(_paged(fn, dims, dev, cache, batch)), batch, n, xp, xs,
+            _dense(fn, dt, dev, gamma, "gamma", (dims.d_c,)),
+            _dense(fn, i32, dev, cu_tokens, "cu_tokens", (batch + 1,)),
+            None if ctx_lens is None else _dense(fn, i32, dev, ctx_lens, "ctx_lens", (batch,)),
+            q, qo)
 
 
 def mla_cache_gather(dims: Dims, cache: PagedCache, cu_rows, first_rows, rows,
                      ws: torch.Tensor = None, stream=None):
     """rows ``[n, d_c + d_rope]``: each sequence's cached rows from first_rows[b] (None: 0) on,
     packed at cu_rows ``[batch + 1]``; int8 rows come back as the values they hold."""
-    fn = "mla_cache_gather"
-    _offsets(fn, cu_rows, "cu_rows")
-    batch = cu_rows.numel() - 1
-    _offsets(fn, first_rows, "first_rows", batch)
-    _paged(fn, dims, cache, batch)
-    _contiguous(fn, rows, "rows", (rows.shape[0], dims.d_c + dims.d_rope), dims.torch_dtype)
-    dev = _same_device(fn, cu_rows, first_rows, rows, cache.pool, cache.block_table, ws)
-    d, c = dims.c(), cache.c()
-    with torch.cuda.device(dev):
-        _ok(fn, lib().mla_cache_gather(
-            ctypes.byref(d), ctypes.byref(c), batch, rows.shape[0], _p(cu_rows), _p(first_rows),
-            _p(rows), _p(ws), ws.numel() * ws.element_size(), _stream(_on(dev, stream))))
+    fn, i32 = "mla_cache_gather", torch.int32
+    dev, n, batch = _device(fn, rows), rows.shape[0], cu_rows.numel() - 1
+    _launch(fn, lib().mla_cache_gather, dev, ws, stream, ctypes.byref(dims.c()),
+            ctypes.byref(_paged(fn, dims, dev, cache, batch)), batch, n,
+            _dense(fn, i32, dev, cu_rows, "cu_rows", (batch + 1,)),
+            None if first_rows is None else _dense(fn, i32, dev, first_rows, "first_rows", (batch,)),
+            _dense(fn, dims.torch_dtype, dev, rows, "rows", (n, dims.d_c + dims.d_rope)))
 
 
 def mla_prompt_attn(dims: Dims, q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, out, lse=None,
@@ -360,28 +362,19 @@ def mla_prompt_attn(dims: Dims, q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, o
     ``[batch + 1]`` int32, out ``[n_q, n_heads, d_v]``, lse ``[n_q, n_heads]``
     fp32 or None.
     """
-    fn = "mla_prompt_attn"
-    _offsets(fn, cu_q, "cu_q")
-    _offsets(fn, cu_k, "cu_k", cu_q.numel())
-    n_q, n_k, n_kv = q_nope.shape[0], k_nope.shape[0], k_nope.shape[1]
-    qn = _heads(fn, dims, q_nope, "q_nope", dims.n_heads, dims.d_nope)
-    qr = _heads(fn, dims, q_rope, "q_rope", dims.n_heads, dims.d_rope)
-    kn = _heads(fn, dims, k_nope, "k_nope", n_kv, dims.d_nope)
-    vv = _heads(fn, dims, v, "v", n_kv, dims.d_v)
-    if k_rope.dim() != 2 or k_rope.shape[1] != dims.d_rope:
-        raise ValueError(f"{fn}: k_rope has shape {tuple(k_rope.shape)}, not [n_k, {dims.d_rope}]")
-    _typed(fn, dims, k_rope, "k_rope")
-    if q_rope.shape[0] != n_q or k_rope.shape[0] != n_k or v.shape[0] != n_k:
-        raise ValueError(f"{fn}: the queries or the keys and values differ in their number of tokens")
-    _contiguous(fn, out, "out", (n_q, dims.n_heads, dims.d_v), dims.torch_dtype)
-    _contiguous(fn, lse, "lse", (n_q, dims.n_heads), torch.float32)
-    dev = _same_device(fn, q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, out, lse, ws)
-    d = dims.c()
-    with torch.cuda.device(dev):
-        _ok(fn, lib().mla_prompt_attn(
-            ctypes.byref(d), cu_q.numel() - 1, n_q, n_k, n_kv, ctypes.byref(qn), ctypes.byref(qr),
-            ctypes.byref(kn), _p(k_rope), k_rope.stride(0), ctypes.byref(vv), _p(cu_q), _p(cu_k),
-            _p(out), _p(lse), _p(ws), ws.numel() * ws.element_size(), _stream(_on(dev, stream))))
+    fn, dt, i32, H = "mla_prompt_attn", dims.torch_dtype, torch.int32, dims.n_heads
+    dev, n_q, n_k, off = _device(fn, q_nope), q_nope.shape[0], k_nope.shape[0], cu_q.shape
+    n_kv = k_nope.shape[1]
+    krp, krs = _rows(fn, dt, dev, k_rope, "k_rope", n_k, dims.d_rope)
+    _launch(fn, lib().mla_prompt_attn, dev, ws, stream, ctypes.byref(dims.c()), off[0] - 1, n_q,
+            n_k, n_kv, ctypes.byref(_heads(fn, dt, dev, q_nope, "q_nope", n_q, H, dims.d_nope)),
+            ctypes.byref(_heads(fn, dt, dev, q_rope, "q_rope", n_q, H, dims.d_rope)),
+            ctypes.byref(_heads(fn, dt, dev, k_nope, "k_nope", n_k, n_kv, dims.d_nope)), krp, krs,
+            ctypes.byref(_heads(fn, dt, dev, v, "v", n_k, n_kv, dims.d_v)),
+            _dense(fn, i32, dev, cu_q, "cu_q", (off[0],)),
+            _dense(fn, i32, dev, cu_k, "cu_k", (off[0],)),
+            _dense(fn, dt, dev, out, "out", (n_q, H, dims.d_v)),
+            None if lse is None else _dense(fn, torch.float32, dev, lse, "lse", (n_q, H)))
 
 
 def mla_noalloc_get_device_error(stream=None) -> int:

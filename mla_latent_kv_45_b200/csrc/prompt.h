@@ -55,19 +55,22 @@ struct PromptItem {
   int k0;    // first key of the sequence in the packed keys
   int lk;    // keys of the sequence
   int see;   // keys that the block's first token sees (may be <= 0); row r sees see + r
-  int pad[3];
 };
 
+// The attention kernel's work counter, and the CTAs that are through with it: the
+// last one sets both back to zero, which mla_workspace_init has them start at.
 struct PromptPlanHeader {
   int items;
-  int next;  // work counter of the attention kernel
+  int next;
+  unsigned done;
 };
 
 struct PromptPlanArgs {
   const int32_t *cu_q, *cu_k;
   int batch, n_q, n_k, tile;
+  int max_items;      // prompt_max_items(n_q, batch, tile); offsets that overlap could ask for more
   PromptPlanHeader *hdr;
-  PromptItem *items;  // [prompt_max_items(n_q, batch, tile)]
+  PromptItem *items;  // [max_items]
   int *err;
 };
 
@@ -75,6 +78,34 @@ struct PromptPlanArgs {
 inline long prompt_max_items(long n_q, long batch, int tile) { return n_q / tile + batch; }
 
 cudaError_t launch_prompt_plan(const PromptPlanArgs &a, cudaStream_t s);
+
+// The rows of sequence b; false when its offsets do not ascend or leave the tensors.
+__device__ __forceinline__ bool prompt_seq(const int32_t *cu_q, const int32_t *cu_k, int n_q,
+                                           int n_k, int b, int &q0, int &lq, int &k0, int &lk) {
+  q0 = cu_q[b];
+  const int q1 = cu_q[b + 1];
+  k0 = cu_k[b];
+  const int k1 = cu_k[b + 1];
+  lq = q1 - q0;
+  lk = k1 - k0;
+  return q0 >= 0 && q1 >= q0 && q1 <= n_q && k0 >= 0 && k1 >= k0 && k1 <= n_k;
+}
+
+// The block of at most `tile` rows that starts at row r of a sequence.
+__device__ __forceinline__ PromptItem prompt_item(int q0, int lq, int k0, int lk, int r, int tile) {
+  PromptItem it{};
+  it.q0 = q0 + r;
+  it.rows = min(tile, lq - r);
+  it.k0 = k0;
+  it.lk = lk;
+  it.see = r + lk - lq + 1;
+  return it;
+}
+
+// Keys that the block's last row sees.
+__device__ __forceinline__ int prompt_keys(const PromptItem &it) {
+  return max(0, min(it.lk, it.see + it.rows - 1));
+}
 
 struct PromptAttnArgs {
   HeadsView q_nope, q_rope, k_nope, v;
@@ -85,6 +116,8 @@ struct PromptAttnArgs {
   float scale;
   PromptPlanHeader *hdr;
   const PromptItem *items;
+  const int32_t *cu_q, *cu_k;
+  int batch;
   void *out;   // [n_q][n_heads][d_v]
   float *lse;  // [n_q][n_heads] or nullptr
   int *err;
@@ -92,6 +125,8 @@ struct PromptAttnArgs {
 
 constexpr int kPromptTileSimt = 16;
 constexpr int kPromptTileSm100 = 256;
+// Up to this many items the sm_100a kernel plans for itself and needs no plan kernel.
+constexpr int kPromptOwnItems = 512;
 
 template <class T>
 cudaError_t launch_prompt_attn_simt(const PromptAttnArgs &a, cudaStream_t s);

@@ -179,7 +179,10 @@ mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, in
   pa.hdr = reinterpret_cast<PromptPlanHeader *>(static_cast<char *>(ws) + kHeaderAt);
   pa.items = reinterpret_cast<PromptItem *>(static_cast<char *>(ws) + kItemsAt);
   pa.err = err_of(ws);
-  MLA_TRY(cuda_ok(launch_prompt_plan(pa, s)));
+  const long max_items = prompt_max_items(n_q, batch, pa.tile);
+  pa.max_items = (int)max_items;
+  if (d.dtype == MLA_FP32 || max_items > kPromptOwnItems)
+    MLA_TRY(cuda_ok(launch_prompt_plan(pa, s)));
   PromptAttnArgs a{};
   a.q_nope = view(q_nope, n_q, d.n_heads, d.d_nope);
   a.q_rope = view(q_rope, n_q, d.n_heads, d.d_rope);
@@ -196,7 +199,10 @@ mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, in
   a.d_nope = d.d_nope;
   a.d_rope = d.d_rope;
   a.d_v = d.d_v;
-  a.max_items = prompt_max_items(n_q, batch, pa.tile);
+  a.max_items = max_items;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.batch = batch;
   a.scale = api::softmax_scale(d);
   a.hdr = pa.hdr;
   a.items = pa.items;

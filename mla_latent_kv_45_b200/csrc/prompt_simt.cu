@@ -362,17 +362,6 @@ __global__ void gather_bf16(GatherArgs a) {
 // the short ones fill the end.
 constexpr int kBins = 1024;
 
-__device__ __forceinline__ bool seq_range(const PromptPlanArgs &a, int b, int &q0, int &lq, int &k0,
-                                          int &lk) {
-  q0 = a.cu_q[b];
-  const int q1 = a.cu_q[b + 1];
-  k0 = a.cu_k[b];
-  const int k1 = a.cu_k[b + 1];
-  lq = q1 - q0;
-  lk = k1 - k0;
-  return q0 >= 0 && q1 >= q0 && q1 <= a.n_q && k0 >= 0 && k1 >= k0 && k1 <= a.n_k;
-}
-
 __global__ void __launch_bounds__(1024) prompt_plan_kernel(PromptPlanArgs a) {
   __shared__ int bins[kBins], warp_tot[32], top_s;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -385,25 +374,20 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(PromptPlanArgs a) {
   auto each = [&](auto &&f) {
     for (int b = tid >> 5; b < a.batch; b += blockDim.x >> 5) {
       int q0, lq, k0, lk;
-      if (!seq_range(a, b, q0, lq, k0, lk)) {
+      if (!prompt_seq(a.cu_q, a.cu_k, a.n_q, a.n_k, b, q0, lq, k0, lk)) {
         if (lane == 0) set_error(a.err, kErrRange);
         continue;
       }
       for (int r = lane * a.tile; r < lq; r += 32 * a.tile) {
-        PromptItem it{};
-        it.q0 = q0 + r;
-        it.rows = min(a.tile, lq - r);
-        it.k0 = k0;
-        it.lk = lk;
-        it.see = r + lk - lq + 1;
-        f(it, max(0, min(lk, it.see + it.rows - 1)));
+        const PromptItem it = prompt_item(q0, lq, k0, lk, r, a.tile);
+        f(it, prompt_keys(it));
       }
     }
   };
   int top = 1;
   for (int b = tid; b < a.batch; b += blockDim.x) {
     int q0, lq, k0, lk;
-    if (seq_range(a, b, q0, lq, k0, lk) && lq > 0) top = max(top, lk);
+    if (prompt_seq(a.cu_q, a.cu_k, a.n_q, a.n_k, b, q0, lq, k0, lk) && lq > 0) top = max(top, lk);
   }
   atomicMax(&top_s, top);
   __syncthreads();
@@ -432,11 +416,13 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(PromptPlanArgs a) {
   const int incl = v + ((tid >> 5) ? warp_tot[(tid >> 5) - 1] : 0);
   bins[tid] = incl - n;
   if (tid == kBins - 1) {
-    a.hdr->items = incl;
-    a.hdr->next = 0;
+    a.hdr->items = min(incl, a.max_items);
   }
   __syncthreads();
-  each([&](const PromptItem &it, int keys) { a.items[atomicAdd(&bins[bin_of(keys)], 1)] = it; });
+  each([&](const PromptItem &it, int keys) {
+    const int at = atomicAdd(&bins[bin_of(keys)], 1);
+    if (at < a.max_items) a.items[at] = it;
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -480,7 +466,7 @@ __global__ void __launch_bounds__(128) prompt_attn_simt(PromptAttnArgs a) {
 #pragma unroll
   for (int j = 0; j < 32; ++j) acc[j] = 0.f;
   const int r_o = tid >> 3, c_o = tid & 7;
-  const int keys = max(0, min(it.lk, it.see + it.rows - 1));
+  const int keys = prompt_keys(it);
   for (int j0 = 0; j0 < keys; j0 += kSimtKeys) {
     const int nk = min(kSimtKeys, keys - j0);
     __syncthreads();

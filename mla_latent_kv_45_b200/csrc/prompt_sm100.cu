@@ -54,7 +54,8 @@ constexpr int kOffV = kOffK + 2 * kKStage;
 constexpr int kOffOut = kOffV + 2 * kVStage;      // [4 output warps][32 rows][128 bytes]
 constexpr int kOffInv = kOffOut + 4 * 4096;       // [2 tiles][128] 1 / row sum
 constexpr int kOffBar = kOffInv + 1024;
-constexpr int kSmemBytes = kOffBar + 1024;
+constexpr int kOffItems = kOffBar + 1024;         // the CTA's own plan
+constexpr int kSmemBytes = kOffItems + kPromptOwnItems * (int)sizeof(PromptItem);
 static_assert(kKBox % 1024 == 0 && kOffOut % 1024 == 0, "swizzled boxes start on 1024 bytes");
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
@@ -151,6 +152,64 @@ __device__ __forceinline__ int tile_steps(const PromptItem &it, int t) {
   return (keys + kKeys - 1) / kKeys;
 }
 
+// Plan of the whole call by one CTA for itself, the same in every CTA: item i of the
+// list is the block with the i-th most keys (ties by sequence and block), so the
+// blocks that take longest start first.  A thread a sequence, then a thread an item;
+// the rank is counted (items^2 / 512 comparisons a thread).  A launch of its own
+// would cost about 6 us, this takes about 1.  Returns the number of items.
+// `scratch`: 4.2 KB of shared memory.
+__device__ __forceinline__ int own_plan(const PromptAttnArgs &a, PromptItem *list, int *scratch) {
+  static_assert(kThreads == kPromptOwnItems, "a thread an item");
+  int *first = scratch;          // [512] items before the sequence
+  int *keys = first + 512;       // [512] of item i, before sorting
+  int *warp_tot = keys + 512;    // [16]
+  const int tid = threadIdx.x, lane = tid & 31;
+  int q0, lq, k0, lk, n = 0;
+  if (tid < a.batch) {
+    if (prompt_seq(a.cu_q, a.cu_k, a.n_q, a.n_k, tid, q0, lq, k0, lk))
+      n = (lq + kPromptTileSm100 - 1) / kPromptTileSm100;
+    else if (blockIdx.x == 0)
+      set_error(a.err, kErrRange);
+  }
+  int v = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  if (lane == 31) warp_tot[tid >> 5] = v;
+  __syncthreads();
+  int before = 0, items = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    before += i < (tid >> 5) ? warp_tot[i] : 0;
+    items += warp_tot[i];
+  }
+  items = min(items, kPromptOwnItems);   // offsets that overlap could ask for more
+  first[tid] = before + v - n;
+  __syncthreads();
+  PromptItem it{};
+  int mine = -1;
+  if (tid < items) {
+    int b = 0;      // the last sequence that starts at item tid or before and is not empty
+#pragma unroll
+    for (int step = kPromptOwnItems / 2; step > 0; step >>= 1)
+      if (b + step < a.batch && first[b + step] <= tid) b += step;
+    prompt_seq(a.cu_q, a.cu_k, a.n_q, a.n_k, b, q0, lq, k0, lk);
+    it = prompt_item(q0, lq, k0, lk, (tid - first[b]) * kPromptTileSm100, kPromptTileSm100);
+    mine = prompt_keys(it);
+  }
+  keys[tid] = mine;
+  __syncthreads();
+  if (tid < items) {
+    int rank = 0;
+    for (int i = 0; i < items; ++i) rank += keys[i] > mine || (keys[i] == mine && i < tid);
+    list[rank] = it;
+  }
+  __syncthreads();
+  return items;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_qn,
                        const __grid_constant__ CUtensorMap tm_qr,
@@ -210,8 +269,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  grid_dep_wait();     // the plan is read from here on
+  grid_dep_wait();     // nothing of the call is read before this
   grid_dep_launch();
+  const bool own = a.max_items <= kPromptOwnItems;
+  PromptItem *const own_items = reinterpret_cast<PromptItem *>(smem + kOffItems);
+  const int items = own ? own_plan(a, own_items, reinterpret_cast<int *>(smem + kOffOut))
+                        : a.hdr->items;
 
   // the k-th work item of this CTA, as a whole warp reads it
   auto take = [&](int k, Work &w) -> bool {
@@ -406,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpLoad) {
     if (lane == 0) {
       const int rep = a.n_heads / a.n_kv_heads;
-      const int items = a.hdr->items, total = items * a.n_heads;
+      const int total = items * a.n_heads;
       const int group_work = items * heads_per_group;
       int gk = 0, gv = 0, nq[2] = {0, 0}, raw[2] = {0, 0};
       bool tail[2] = {false, false};
@@ -433,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.head = -1;
         if (idx < total) {
           const int g = idx / group_work, r = idx % group_work;
-          w.it = a.items[r / heads_per_group];
+          w.it = own ? own_items[r / heads_per_group] : a.items[r / heads_per_group];
           w.head = g * heads_per_group + r % heads_per_group;
         }
         const int slot = k % kSched;
@@ -480,6 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (ok && !bars->abort && gv < gk) load_v();
+      // no CTA asks for work any more once all have been here
+      if (atomicInc(&a.hdr->done, gridDim.x - 1) == gridDim.x - 1) a.hdr->next = 0;
       if (bars->abort) {
         // what is in flight must land before the CTA ends
         for (int g = max(0, gk - 2); g < gk; ++g) drain_bar(&bars->k_full[g & 1], (g >> 1) & 1);

@@ -60,6 +60,53 @@ def test_many_sequences():
     go(dims_of(V2, 2, BF), new, total, 1)
 
 
+def test_more_sequences_than_a_block_plans_for_itself():
+    new = [(13 * i) % 29 for i in range(700)] + [700]
+    total = [n + (5 * i) % 40 for i, n in enumerate(new)]
+    go(dims_of(V2, 1, BF), new, total, 1)
+
+
+@pytest.mark.parametrize("batch", [3, 1200])
+def test_offsets_that_overlap(batch):
+    """Descending offsets make sequences overlap: more blocks than the tokens have.  The error
+    word is set, nothing outside the tensors is touched, and the next call is right."""
+    dims = dims_of(V2, 1, BF)
+    t = attn_inputs(dims, 300, 300, 1, 31)
+    ws = workspace(dims, batch, 300)
+    guard = torch.full((4096,), 7, dtype=torch.uint8, device="cuda")
+    cu = [0, 300] * (batch // 2) + [0, 300][:batch % 2 + 1]
+    out = torch.empty(300, 1, 128, dtype=BF, device="cuda")
+    L.mla_prompt_attn(dims, t["q_nope"], t["q_rope"], t["k_nope"], t["k_rope"], t["v"], i32(cu),
+                      i32(cu), out, None, ws)
+    assert L.mla_get_device_error(ws) == 6
+    assert (guard == 7).all()
+    pad = [0] * batch + [300]
+    run_attn(dims, t, pad, pad, ws=ws)
+    out, lse = run_attn(dims, t, [0, 300], [0, 300])
+    check_attn(dims, t, [0, 300], [0, 300], out, lse)
+
+
+def test_refusals_on_the_device():
+    dims = dims_of(V2, 2, BF)
+    good = attn_inputs(dims, 20, 20, 1, 33)
+    ws = workspace(dims, 1, 20)
+    out, lse = torch.zeros(20, 2, 128, dtype=BF, device="cuda"), torch.zeros(20, 2, device="cuda")
+    cu = i32([0, 20])
+    base = dict(good, cu_q=cu, cu_k=cu, out=out, lse=lse, ws=ws)
+    L.mla_prompt_attn(dims, **base)
+    for name, bad in (("q_nope", good["q_nope"].float()), ("q_nope", good["q_nope"][:, :1]),
+                      ("q_rope", good["q_rope"][:19]), ("k_rope", good["k_rope"][:, ::2]),
+                      ("k_rope", good["k_rope"].cpu()), ("v", good["v"][:19]),
+                      ("v", good["v"].transpose(1, 2)), ("cu_q", cu.long()), ("cu_k", i32([0, 1, 2])),
+                      ("out", out.transpose(0, 1)), ("lse", lse.to(BF)), ("lse", lse[:, :1]),
+                      ("ws", None), ("ws", ws.cpu())):
+        with pytest.raises(ValueError):
+            L.mla_prompt_attn(dims, **{**base, name: bad})
+    with pytest.raises(L.MlaError) as e:
+        L.mla_prompt_attn(dims, **{**base, "ws": ws[:16]})
+    assert e.value.status == 4
+
+
 def test_queries_that_see_no_key():
     """lq > lk: the first lq - lk queries see nothing and get zeros and -inf."""
     new, total = [200, 5, 130, 300], [72, 0, 1, 20]
