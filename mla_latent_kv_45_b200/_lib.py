@@ -288,23 +288,27 @@ def _paged(fn: str, dims: Dims, dev: int, cache: PagedCache, batch: int) -> _Cac
                   table, None if cache.seq_lens is None else cache.seq_lens.data_ptr())
 
 
+# The current stream's address without a Stream object around it, where torch has that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _launch(fn: str, call, dev: int, ws: torch.Tensor, stream, *args):
     """Calls the library on `stream` (default: the tensors' device's current one), with the
     tensors' device current."""
     if ws is None or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"{fn}: ws is not a contiguous tensor on cuda:{dev}")
-    if stream is not None and stream.device_index != dev:
+    if stream is None:
+        handle = _raw_stream(dev)
+    elif stream.device_index != dev:
         raise ValueError(f"{fn}: stream on {stream.device}, tensors on cuda:{dev}")
-    here = torch.cuda.current_device()
-    if here != dev:
-        torch.cuda.set_device(dev)
-    try:
-        if stream is None:
-            stream = torch.cuda.current_stream()
-        st = call(*args, ws.data_ptr(), ws.nbytes, stream.cuda_stream)
-    finally:
-        if here != dev:
-            torch.cuda.set_device(here)
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = call(*args, ws.data_ptr(), ws.nbytes, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args, ws.data_ptr(), ws.nbytes, handle)
     if st != 0:
         raise MlaError(fn, st)
 
