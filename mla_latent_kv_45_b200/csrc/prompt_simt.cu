@@ -125,12 +125,14 @@ __global__ void prompt_append_f32(PromptAppendArgs a, RopeParams rp) {
   }
 }
 
-constexpr int kSlab = 16;  // heads a warp rotates per round: 2 units of 8 pairs a lane
+constexpr int kSlab = 32;  // heads a warp rotates per round: 4 units of 8 pairs a lane
 
 // A token is the work of `group` warps: the last one normalises, rotates and
 // writes the cache row, the others rotate the heads.  Every warp finds its
 // token's sequence and evaluates the 32 angles (one a lane) by itself, so
-// nothing is shared between warps and nothing waits.
+// nothing is shared between warps and nothing waits.  Bound by the bytes (a token
+// of 128 heads moves 34.5 KB), so a warp asks for its first 4 KB before it looks
+// for the sequence.
 //
 // A unit is 8 rotation pairs = two 16-byte vectors of a 64-wide head:
 // interleaved pairs (vectors 2u, 2u + 1) or split halves (vectors u, u + 4).  Lane l
@@ -141,8 +143,34 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x / 32 / group) + warp / group;
   const int role = warp % group;
+  const int u = lane & 3;
+  const int v0 = rp.half ? u : 2 * u, v1 = rp.half ? u + 4 : 2 * u + 1;
   grid_dep_wait();
   if (t >= a.n_tokens) return;
+  uint4 p[4], r[4];
+  const bf16 *q = static_cast<const bf16 *>(a.q.ptr) + t * a.q.token;
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int h = h0 + 8 * k + (lane >> 2);
+      if (h < a.n_heads) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(q + h * a.q.head);
+        p[k] = src[v0];
+        r[k] = src[v1];
+      }
+    }
+  };
+  uint4 xc[2], xr[2];
+  if (role < group - 1) {
+    load(role * kSlab);
+  } else {
+    const uint4 *x =
+        reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(a.x) + t * a.x_stride);
+    xc[0] = x[lane];
+    xc[1] = x[32 + lane];
+    xr[0] = x[64 + v0];
+    xr[1] = x[64 + v1];
+  }
   const int b = warp_find_seq(a.cu, a.batch, t);
   if (b < 0) {
     if (lane == 0 && t >= a.cu[0] && t < a.cu[a.batch]) set_error(a.err, kErrRange);
@@ -155,14 +183,12 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
   }
   float cf, sf;
   rope_cos_sin((int)pos, rp.theta[lane], cf, sf);
-  const int u = lane & 3;
   float cs[8], sn[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     cs[i] = __shfl_sync(0xffffffffu, cf, 8 * u + i);
     sn[i] = __shfl_sync(0xffffffffu, sf, 8 * u + i);
   }
-  const int v0 = rp.half ? u : 2 * u, v1 = rp.half ? u + 4 : 2 * u + 1;
   auto turn = [&](uint4 &p, uint4 &r) {
     float f[16];
     unpack8(p, f);
@@ -179,21 +205,10 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
   };
 
   if (role < group - 1) {
-    const bf16 *q = static_cast<const bf16 *>(a.q.ptr) + t * a.q.token;
     bf16 *qo = static_cast<bf16 *>(const_cast<void *>(a.q_out.ptr)) + t * a.q_out.token;
-    for (int h0 = role * kSlab; h0 < a.n_heads; h0 += (group - 1) * kSlab) {
-      uint4 p[2], r[2];
+    for (int h0 = role * kSlab; h0 < a.n_heads;) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int h = h0 + 8 * k + (lane >> 2);
-        if (h < a.n_heads) {
-          const uint4 *src = reinterpret_cast<const uint4 *>(q + h * a.q.head);
-          p[k] = src[v0];
-          r[k] = src[v1];
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < 4; ++k) {
         const int h = h0 + 8 * k + (lane >> 2);
         if (h < a.n_heads) {
           turn(p[k], r[k]);
@@ -202,30 +217,27 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
           dst[v1] = r[k];
         }
       }
+      h0 += (group - 1) * kSlab;
+      load(h0);
     }
     return;
   }
 
-  // the cache row: lane l holds latent values [16 l, 16 l + 16), lanes 0..3 also
-  // one unit of k_R
+  // the cache row: lane l holds latent values [8 l, 8 l + 8) and [256 + 8 l, 256 + 8 l + 8),
+  // lanes 0..3 also one unit of k_R
   const int page = page_of(a.block_table, a.max_pages, a.num_pages, a.page_size, b, pos);
   if (page < 0) {
     if (lane == 0) set_error(a.err, kErrRange);
     return;
   }
-  const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(a.x) + t * a.x_stride);
   const uint4 *g = static_cast<const uint4 *>(a.gamma);
   float c[16], gm[16];
-  unpack8(x[2 * lane], c);
-  unpack8(x[2 * lane + 1], c + 8);
-  unpack8(g[2 * lane], gm);
-  unpack8(g[2 * lane + 1], gm + 8);
-  uint4 kp = make_uint4(0, 0, 0, 0), kr = kp;
-  if (lane < 4) {
-    kp = x[64 + v0];
-    kr = x[64 + v1];
-    turn(kp, kr);
-  }
+  unpack8(xc[0], c);
+  unpack8(xc[1], c + 8);
+  unpack8(g[lane], gm);
+  unpack8(g[32 + lane], gm + 8);
+  uint4 kp = xr[0], kr = xr[1];
+  turn(kp, kr);
   const long slot = (long)page * a.page_size + pos % a.page_size;
   if (!kI8) {
     float ss = 0.f;
@@ -235,8 +247,8 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
 #pragma unroll
     for (int i = 0; i < 16; ++i) c[i] = gm[i] * (c[i] * inv);
     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<bf16 *>(a.pool) + slot * 576);
-    dst[2 * lane] = pack8(c);
-    dst[2 * lane + 1] = pack8(c + 8);
+    dst[lane] = pack8(c);
+    dst[32 + lane] = pack8(c + 8);
     if (lane < 4) {
       dst[64 + v0] = kp;
       dst[64 + v1] = kr;
@@ -273,7 +285,8 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
       w[i >> 2] |= (uint32_t)(q & 255) << (8 * (i & 3));
     }
     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.pool) + slot * 656);
-    dst[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint2 *>(dst)[lane] = make_uint2(w[0], w[1]);
+    reinterpret_cast<uint2 *>(dst)[32 + lane] = make_uint2(w[2], w[3]);
     if (lane < 4) {
       dst[32 + v0] = kp;
       dst[32 + v1] = kr;
@@ -286,70 +299,99 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
 // Cache gather: packed rows out of the pages
 // ---------------------------------------------------------------------------
 
-// Source row (page * page_size + slot) of packed row t by one warp: -1 when t
-// belongs to no sequence, -2 when its place in the cache is out of range.
-__device__ __forceinline__ long gather_source(const GatherArgs &a, int t) {
-  const int b = warp_find_seq(a.cu, a.batch, t);
-  if (b < 0) return t >= a.cu[0] && t < a.cu[a.batch] ? -2 : -1;
-  const long pos = (long)(a.first ? a.first[b] : 0) + (t - a.cu[b]);
-  const int page = page_of(a.block_table, a.max_pages, a.num_pages, a.page_size, b, pos);
-  return page < 0 ? -2 : (long)page * a.page_size + pos % a.page_size;
-}
-
 // One warp a row.  A row without a place in the cache is zeroed.
 __global__ void gather_f32(GatherArgs a, int row) {
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   grid_dep_wait();
   if (t >= a.n_rows) return;
-  const long src = gather_source(a, t);
-  if (src == -1) return;
+  const int b = warp_find_seq(a.cu, a.batch, t);
+  long src = -2;
+  if (b >= 0) {
+    const long pos = (long)(a.first ? a.first[b] : 0) + (t - a.cu[b]);
+    const int page = page_of(a.block_table, a.max_pages, a.num_pages, a.page_size, b, pos);
+    if (page >= 0) src = (long)page * a.page_size + pos % a.page_size;
+  } else if (t < a.cu[0] || t >= a.cu[a.batch]) {
+    return;
+  }
   if (src < 0 && lane == 0) set_error(a.err, kErrRange);
   const float *p = static_cast<const float *>(a.pool) + (src < 0 ? 0 : src) * row;
   float *o = static_cast<float *>(a.rows) + (long)t * row;
   for (int i = lane; i < row; i += 32) o[i] = src < 0 ? 0.f : p[i];
 }
 
-// 16 int8 codes times the power-of-two scale s, as 16 bf16 values (exact).
-__device__ __forceinline__ void codes16(const uint4 &in, float s, uint4 &lo, uint4 &hi) {
-  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-  float f[16];
+// 8 int8 codes times the power-of-two scale s, as 8 bf16 values.  The byte q + 128
+// in the low mantissa bits of 2^23 makes the float 2^23 + q + 128, so one fma gives
+// q s, which has 8 significant bits at most: exact in fp32 and in bf16.
+__device__ __forceinline__ uint4 codes8(const uint2 &in, float s) {
+  const float bias = -8388736.0f * s;
+  const uint32_t w[2] = {in.x ^ 0x80808080u, in.y ^ 0x80808080u};
+  float f[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    f[i] = (float)static_cast<int8_t>(w[i >> 2] >> (8 * (i & 3))) * s;
-  lo = pack8(f);
-  hi = pack8(f + 8);
+  for (int i = 0; i < 8; ++i)
+    f[i] = fmaf(__uint_as_float(__byte_perm(w[i >> 2], 0x4B000000u, 0x7540u + (i & 3))), s, bias);
+  return pack8(f);
 }
 
+constexpr int kGatherRows = 2;  // rows of a warp, all asked for before the first is written
+
+// One warp two rows (one or four: 5 % slower for bf16 or for int8 rows): a pass of reads and writes, bound by the bytes.
 template <bool kI8>
 __global__ void gather_bf16(GatherArgs a) {
-  const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
+  const int t0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kGatherRows;
   grid_dep_wait();
-  if (t >= a.n_rows) return;
-  const long src = gather_source(a, t);
-  if (src == -1) return;
-  uint4 *o = reinterpret_cast<uint4 *>(static_cast<bf16 *>(a.rows) + (long)t * 576);
-  if (src < 0) {
-    if (lane == 0) set_error(a.err, kErrRange);
-    for (int i = lane; i < 72; i += 32) o[i] = make_uint4(0, 0, 0, 0);
-    return;
+  if (t0 >= a.n_rows) return;
+  // the first row's sequence by the whole warp, then lane i looks for row i's place
+  const int b0 = warp_find_seq(a.cu, a.batch, t0);
+  long mine = -1;
+  const int t = t0 + lane;
+  if (lane < kGatherRows && t < a.n_rows) {
+    int b = max(b0, 0);
+    while (b + 1 < a.batch && t >= a.cu[b + 1]) ++b;
+    if (t >= a.cu[b] && t < a.cu[b + 1]) {
+      const long pos = (long)(a.first ? a.first[b] : 0) + (t - a.cu[b]);
+      const int page = page_of(a.block_table, a.max_pages, a.num_pages, a.page_size, b, pos);
+      mine = page < 0 ? -2 : (long)page * a.page_size + pos % a.page_size;
+    } else if (t >= a.cu[0] && t < a.cu[a.batch]) {
+      mine = -2;
+    }
+    if (mine == -2) set_error(a.err, kErrRange);
   }
-  if (kI8) {
-    const uint8_t *p = static_cast<const uint8_t *>(a.pool) + src * 656;
+  long src[kGatherRows];
+#pragma unroll
+  for (int i = 0; i < kGatherRows; ++i) src[i] = __shfl_sync(0xffffffffu, mine, i);
+  // lane l writes vectors l, 32 + l and (l < 8) 64 + l of a row, whole lines at a time
+  uint4 x[kGatherRows][3];
+  uint2 y[kGatherRows][2];
+  float s[kGatherRows];
+#pragma unroll
+  for (int i = 0; i < kGatherRows; ++i) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) x[i][k] = make_uint4(0, 0, 0, 0);
+    y[i][0] = y[i][1] = make_uint2(0x80808080u, 0x80808080u);
+    s[i] = 0.f;
+    if (src[i] < 0) continue;
+    const uint8_t *p = static_cast<const uint8_t *>(a.pool) + src[i] * (kI8 ? 656 : 1152);
     const uint4 *v = reinterpret_cast<const uint4 *>(p);
-    const uint4 codes = v[lane];
-    const uint4 kr = lane < 8 ? v[32 + lane] : make_uint4(0, 0, 0, 0);
-    const float s = *reinterpret_cast<const float *>(p + 640);
-    uint4 lo, hi;
-    codes16(codes, s, lo, hi);
-    o[2 * lane] = lo;
-    o[2 * lane + 1] = hi;
-    if (lane < 8) o[64 + lane] = kr;
-  } else {
-    const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(a.pool) + src * 576);
-    const uint4 x = v[lane], y = v[32 + lane];
-    if (lane < 8) o[64 + lane] = v[64 + lane];
-    o[lane] = x;
-    o[32 + lane] = y;
+    if (kI8) {
+      const uint2 *c = reinterpret_cast<const uint2 *>(p);
+      y[i][0] = c[lane];
+      y[i][1] = c[32 + lane];
+      if (lane < 8) x[i][2] = v[32 + lane];
+      s[i] = *reinterpret_cast<const float *>(p + 640);
+    } else {
+      x[i][0] = v[lane];
+      x[i][1] = v[32 + lane];
+      if (lane < 8) x[i][2] = v[64 + lane];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kGatherRows; ++i) {
+    if (src[i] == -1) continue;      // a row that no sequence has; one without a page is zeroed
+    uint4 *o = reinterpret_cast<uint4 *>(static_cast<bf16 *>(a.rows) + (long)(t0 + i) * 576);
+    o[lane] = kI8 ? codes8(y[i][0], s[i]) : x[i][0];
+    o[32 + lane] = kI8 ? codes8(y[i][1], s[i]) : x[i][1];
+    if (lane < 8) o[64 + lane] = x[i][2];
   }
 }
 
@@ -553,7 +595,7 @@ cudaError_t launch_gather_f32(const GatherArgs &a, int row, cudaStream_t s) {
 }
 
 cudaError_t launch_gather_bf16(const GatherArgs &a, bool int8_rows, cudaStream_t s) {
-  const dim3 grid((a.n_rows + 7) / 8);
+  const dim3 grid((a.n_rows + 8 * kGatherRows - 1) / (8 * kGatherRows));
   return int8_rows ? launch_pdl(gather_bf16<true>, grid, dim3(256), 0, s, a)
                    : launch_pdl(gather_bf16<false>, grid, dim3(256), 0, s, a);
 }
