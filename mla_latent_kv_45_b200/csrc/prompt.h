@@ -112,6 +112,7 @@ struct PromptAttnArgs {
   const void *k_rope;
   int64_t k_rope_stride;
   int n_q, n_k, n_heads, n_kv_heads, d_nope, d_rope, d_v;
+  int pack_log2;   // sm_100a: heads of a group that share a tile (log2)
   long max_items;
   float scale;
   PromptPlanHeader *hdr;
@@ -124,7 +125,7 @@ struct PromptAttnArgs {
 };
 
 constexpr int kPromptTileSimt = 16;
-constexpr int kPromptTileSm100 = 256;
+constexpr int kPromptTileSm100 = 256;   // rows of an item: (token, head) pairs
 // Up to this many items the sm_100a kernel plans for itself and needs no plan kernel.
 constexpr int kPromptOwnItems = 512;
 

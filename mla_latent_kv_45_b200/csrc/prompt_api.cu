@@ -21,8 +21,25 @@ using api::aligned4;
 
 mla_status cuda_ok(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
 
-int tile_rows(const mla_dims &d) {
-  return d.dtype == MLA_BF16 ? kPromptTileSm100 : kPromptTileSimt;
+// log2 of the heads that share a tile: the largest power of two that divides a
+// group of `rep` query heads, 128 at most.
+int pack_log2(int rep) {
+  int lg = 0;
+  while (lg < 7 && rep % (2 << lg) == 0) ++lg;
+  return lg;
+}
+
+// Tokens of an item with groups of `rep` heads.
+int tile_tokens(const mla_dims &d, int rep) {
+  return d.dtype == MLA_BF16 ? kPromptTileSm100 >> pack_log2(rep) : kPromptTileSimt;
+}
+
+// ... the fewest that any grouping of the heads has.
+int least_tile_tokens(const mla_dims &d) {
+  int least = tile_tokens(d, 1);
+  for (int rep = 2; rep <= d.n_heads; ++rep)
+    if (d.n_heads % rep == 0 && tile_tokens(d, rep) < least) least = tile_tokens(d, rep);
+  return least;
 }
 
 // The error word and the plan header share the first 256 bytes (the part that
@@ -30,7 +47,7 @@ int tile_rows(const mla_dims &d) {
 constexpr size_t kItemsAt = 256, kHeaderAt = 64;
 
 size_t prompt_ws_bytes(const mla_dims &d, int batch, int n_tokens) {
-  return kItemsAt + sizeof(PromptItem) * (size_t)prompt_max_items(n_tokens, batch, tile_rows(d));
+  return kItemsAt + sizeof(PromptItem) * (size_t)prompt_max_items(n_tokens, batch, least_tile_tokens(d));
 }
 
 mla_status check_ws(const void *ws, size_t ws_bytes, size_t need) {
@@ -175,7 +192,8 @@ mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, in
   pa.batch = batch;
   pa.n_q = n_q;
   pa.n_k = n_k;
-  pa.tile = tile_rows(d);
+  const int rep = d.n_heads / n_kv_heads;
+  pa.tile = tile_tokens(d, rep);
   pa.hdr = reinterpret_cast<PromptPlanHeader *>(static_cast<char *>(ws) + kHeaderAt);
   pa.items = reinterpret_cast<PromptItem *>(static_cast<char *>(ws) + kItemsAt);
   pa.err = err_of(ws);
@@ -196,6 +214,7 @@ mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, in
   a.n_k = n_k;
   a.n_heads = d.n_heads;
   a.n_kv_heads = n_kv_heads;
+  a.pack_log2 = pack_log2(rep);
   a.d_nope = d.d_nope;
   a.d_rope = d.d_rope;
   a.d_v = d.d_v;

@@ -5,8 +5,11 @@
 // one pass over the keys with a running maximum m and sum l per row
 // ("从零理解 MLA", 解耦 RoPE MLADecoupledRoPE.forward).
 //
-// One work item is 256 query rows of one head: two 128-row tiles that share
-// every key and value in shared memory.  Per step of 80 keys a tile costs
+// One work item is 256 query rows: two 128-row tiles that share every key and value
+// in shared memory.  A row is a (token, head) pair.  With one key head per query head
+// they are 256 tokens of one head; grouped heads are packed, 2^lg heads of the group
+// (the largest power of two that divides it, 128 at most) of 256 / 2^lg tokens, so a
+// key head is read once for all of them and short chunks still fill a tile.  Per step of 80 keys a tile costs
 // S = Q K^T (K = 192, the two score terms are one product) and O += P V.
 //  * 80 keys a step, because TMEM then holds S (80 columns) beside P (bf16, 40
 //    columns) and O (128) of both tiles: 496 of 512 columns.  A step's scores are
@@ -52,8 +55,8 @@ constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + 2 * kQTile;
 constexpr int kOffV = kOffK + 2 * kKStage;
 constexpr int kOffOut = kOffV + 2 * kVStage;      // [4 output warps][32 rows][128 bytes]
-constexpr int kOffInv = kOffOut + 4 * 4096;       // [2 tiles][128] 1 / row sum
-constexpr int kOffBar = kOffInv + 1024;
+constexpr int kOffInv = kOffOut + 4 * 4096;       // [2 tiles][128] 1 / row sum, then lse
+constexpr int kOffBar = kOffInv + 2048;
 constexpr int kOffItems = kOffBar + 1024;         // the CTA's own plan
 constexpr int kSmemBytes = kOffItems + kPromptOwnItems * (int)sizeof(PromptItem);
 static_assert(kKBox % 1024 == 0 && kOffOut % 1024 == 0, "swizzled boxes start on 1024 bytes");
@@ -141,14 +144,16 @@ __device__ __forceinline__ void weights16(const float *v, uint64_t scale2, uint6
   }
 }
 
-// Rows of tile t of an item, and the steps that its last row's keys take.
-__device__ __forceinline__ int tile_rows(const PromptItem &it, int t) {
-  return max(0, min(kRows, it.rows - t * kRows));
+// Tokens of tile t of an item (a tile has 128 >> lg of them, each with 1 << lg heads),
+// and the steps that its last token's keys take.
+__device__ __forceinline__ int tile_tokens(const PromptItem &it, int t, int lg) {
+  const int tt = kRows >> lg;
+  return max(0, min(tt, it.rows - t * tt));
 }
-__device__ __forceinline__ int tile_steps(const PromptItem &it, int t) {
-  const int rows = tile_rows(it, t);
-  if (rows == 0) return 0;
-  const int keys = max(0, min(it.lk, it.see + t * kRows + rows - 1));
+__device__ __forceinline__ int tile_steps(const PromptItem &it, int t, int lg) {
+  const int toks = tile_tokens(it, t, lg);
+  if (toks == 0) return 0;
+  const int keys = max(0, min(it.lk, it.see + t * (kRows >> lg) + toks - 1));
   return (keys + kKeys - 1) / kKeys;
 }
 
@@ -163,11 +168,11 @@ __device__ __forceinline__ int own_plan(const PromptAttnArgs &a, PromptItem *lis
   int *first = scratch;          // [512] items before the sequence
   int *keys = first + 512;       // [512] of item i, before sorting
   int *warp_tot = keys + 512;    // [16]
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, tile = kPromptTileSm100 >> a.pack_log2;
   int q0, lq, k0, lk, n = 0;
   if (tid < a.batch) {
     if (prompt_seq(a.cu_q, a.cu_k, a.n_q, a.n_k, tid, q0, lq, k0, lk))
-      n = (lq + kPromptTileSm100 - 1) / kPromptTileSm100;
+      n = (lq + tile - 1) / tile;
     else if (blockIdx.x == 0)
       set_error(a.err, kErrRange);
   }
@@ -196,7 +201,7 @@ __device__ __forceinline__ int own_plan(const PromptAttnArgs &a, PromptItem *lis
     for (int step = kPromptOwnItems / 2; step > 0; step >>= 1)
       if (b + step < a.batch && first[b + step] <= tid) b += step;
     prompt_seq(a.cu_q, a.cu_k, a.n_q, a.n_k, b, q0, lq, k0, lk);
-    it = prompt_item(q0, lq, k0, lk, (tid - first[b]) * kPromptTileSm100, kPromptTileSm100);
+    it = prompt_item(q0, lq, k0, lk, (tid - first[b]) * tile, tile);
     mine = prompt_keys(it);
   }
   keys[tid] = mine;
@@ -221,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Bars *bars = reinterpret_cast<Bars *>(smem + kOffBar);
   const Ctx ctx{bars, a.err};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lg = a.pack_log2, tt = kRows >> lg;   // heads a token has in a tile, tokens of a tile
 
   // The swizzled boxes need a 1024-byte boundary, which the dynamic shared memory
   // starts on (there is no static part in front of it).
@@ -305,10 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Work w;
     for (int k = 0; ok && take(k, w); ++k) {
-      const int rows = tile_rows(w.it, t);
-      const int steps = tile_steps(w.it, t);
+      const int steps = tile_steps(w.it, t, lg);
       if (steps == 0) continue;
-      const int see = max(0, min(w.it.lk, w.it.see + t * kRows + row));   // keys this row sees
+      const int see = max(0, min(w.it.lk, w.it.see + t * tt + (row >> lg)));   // keys this row sees
       const int see_warp = __shfl_sync(0xffffffffu, see, 0);              // ... the warp's fewest
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < steps; ++j, ++ns) {
@@ -396,12 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ni > 0) ok = wait_all(&bars->o_free[t], (ni - 1) & 1);
       if (!ok) break;
       ++ni;
-      inv_s[row] = 1.f / l;
+      inv_s[row] = see > 0 ? 1.f / l : 0.f;
+      inv_s[256 + row] = see > 0 ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->l_full[t]);
-      if (row < rows && a.lse)
-        a.lse[(long)(w.it.q0 + t * kRows + row) * a.n_heads + w.head] =
-            see > 0 ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
   } else if (warp < kWarpOut + 4) {
     // ---------- output: O / row sum, while the softmax warps go on with the next item
@@ -415,10 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok && take(k, w); ++k) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int rows = tile_rows(w.it, t), steps = tile_steps(w.it, t);
-        if (rows == 0) continue;
-        const int see = min(w.it.lk, w.it.see + t * kRows + row);
-        const long tok = w.it.q0 + t * kRows + warp_row;   // of the warp's first row
+        const int toks = tile_tokens(w.it, t, lg), steps = tile_steps(w.it, t, lg);
+        if (toks == 0) continue;
+        const bool sees = min(w.it.lk, w.it.see + t * tt + (row >> lg)) > 0;
+        // (token, head) number of the tile's row r, from that of its first
+        const long at0 = (long)(w.it.q0 + t * tt) * a.n_heads + w.head;
+        auto at = [&](int r) { return at0 + (long)(r >> lg) * a.n_heads + (r & ((1 << lg) - 1)); };
         float inv = 0.f;
         if (steps > 0) {
           ok = wait_all(&bars->l_full[t], no[t] & 1) && wait_all(&bars->o_full[t], no[t] & 1);
@@ -426,9 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++no[t];
           tc_fence_after();
           inv = inv_s[128 * t + row];
-        } else if (row < rows && a.lse) {      // no row of the tile sees a key
-          a.lse[(tok + lane) * a.n_heads + w.head] = -INFINITY;
         }
+        if ((row >> lg) < toks && a.lse)
+          a.lse[at(row)] = steps > 0 ? inv_s[256 + 128 * t + row] : -INFINITY;
         const uint32_t o_addr = tmem + lane_off + kTmemO + 128 * t;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
@@ -444,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t x[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                x[e] = steps > 0 && see > 0
+                x[e] = steps > 0 && sees
                            ? pack2(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv) : 0u;
               *reinterpret_cast<uint4 *>(stage + lane * 128 + (((4 * q + i) ^ (lane & 7)) << 4)) =
                   make_uint4(x[0], x[1], x[2], x[3]);
@@ -453,23 +458,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (h == 1 && steps > 0) tc_fence_before();
           __syncwarp();
           if (h == 1 && steps > 0 && lane == 0) mbar_arrive(&bars->o_free[t]);
-          bf16 *dst = static_cast<bf16 *>(a.out) + (tok * a.n_heads + w.head) * 128 + 64 * h;
+          bf16 *dst = static_cast<bf16 *>(a.out) + 64 * h;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = 4 * i + (lane >> 3), u = lane & 7;
             const uint4 x =
                 *reinterpret_cast<const uint4 *>(stage + r * 128 + ((u ^ (r & 7)) << 4));
-            if (warp_row + r < rows)
-              *reinterpret_cast<uint4 *>(dst + (long)r * a.n_heads * 128 + 8 * u) = x;
+            if (((warp_row + r) >> lg) < toks)
+              *reinterpret_cast<uint4 *>(dst + at(warp_row + r) * 128 + 8 * u) = x;
           }
           __syncwarp();
         }
       }
     }
   } else if (warp == kWarpLoad) {
-    if (lane == 0) {
+    if (elect_one()) {
       const int rep = a.n_heads / a.n_kv_heads;
-      const int total = items * a.n_heads;
+      const int total = items * (a.n_heads >> lg);
       const int group_work = items * heads_per_group;
       int gk = 0, gv = 0, nq[2] = {0, 0}, raw[2] = {0, 0};
       bool tail[2] = {false, false};
@@ -497,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (idx < total) {
           const int g = idx / group_work, r = idx % group_work;
           w.it = own ? own_items[r / heads_per_group] : a.items[r / heads_per_group];
-          w.head = g * heads_per_group + r % heads_per_group;
+          w.head = (g * heads_per_group + r % heads_per_group) << lg;
         }
         const int slot = k % kSched;
         if (k >= kSched && !wait_bar(ctx, &bars->w_empty[slot], ((k / kSched) - 1) & 1)) break;
@@ -506,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w.head < 0) break;
         idx = (int)gridDim.x + atomicAdd(&a.hdr->next, 1);
         const int kv = w.head / rep;
-        const int n_t[2] = {tile_steps(w.it, 0), tile_steps(w.it, 1)};
+        const int n_t[2] = {tile_steps(w.it, 0, lg), tile_steps(w.it, 1, lg)};
         const int n = max(n_t[0], n_t[1]);
         // Q of tile t, once the item before has its last scores
         auto load_q = [&](int t) -> bool {
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (nq[t] > 0 && !wait_bar(ctx, &bars->q_empty[t], (nq[t] - 1) & 1)) return false;
           ++nq[t];
           uint8_t *q = smem + kOffQ + t * kQTile;
-          const int row = w.it.q0 + t * kRows;
+          const int row = w.it.q0 + t * tt;
           mbar_expect_tx(&bars->q_full[t], kQTile);
           tma_load_3d(q, &tm_qn, 0, w.head, row, &bars->q_full[t]);
           tma_load_3d(q + kQBox, &tm_qn, 64, w.head, row, &bars->q_full[t]);
@@ -564,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ph[2] = {0, 0};
     Work w;
     for (int k = 0; take(k, w); ++k) {
-      const int n = max(tile_steps(w.it, 0), tile_steps(w.it, 1));
+      const int n = max(tile_steps(w.it, 0, lg), tile_steps(w.it, 1, lg));
       const int left = w.it.lk - (n - 1) * kKeys;   // keys of the item's last step
       if (n > 0 && left < kKeys) {
         const int u = (g0 + n - 1) & 1;
@@ -601,8 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Work w = bars->work[slot];
           mbar_arrive(&bars->w_empty[slot]);
           if (w.head < 0) return false;
-          n_t = tile_steps(w.it, t);
-          n = max(n_t, tile_steps(w.it, t ^ 1));
+          n_t = tile_steps(w.it, t, lg);
+          n = max(n_t, tile_steps(w.it, t ^ 1, lg));
           if (n > 0) return true;
         }
       };
@@ -709,15 +714,15 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// Map of a packed [tokens][heads][width] bf16 view; box = 64 columns of one head
-// of `box_tokens` tokens.  Tokens past the end read as zeros.
+// Map of a packed [tokens][heads][width] bf16 view; box = 64 columns of box_heads
+// heads of box_tokens tokens, heads running faster.  Tokens past the end read as zeros.
 bool map_heads(CUtensorMap *m, const HeadsView &v, int tokens, int heads, int width,
-               int box_tokens) {
+               int box_heads, int box_tokens) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {(cuuint64_t)v.head * 2, (cuuint64_t)v.token * 2};
-  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_tokens}, estr[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens}, estr[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(v.ptr), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -744,13 +749,14 @@ cudaError_t launch_prompt_attn(const PromptAttnArgs &a, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   CUtensorMap qn, qr, kn, kr, v;
-  if (!map_heads(&qn, a.q_nope, a.n_q, a.n_heads, 128, kRows) ||
-      !map_heads(&qr, a.q_rope, a.n_q, a.n_heads, 64, kRows))
+  const int pack = 1 << a.pack_log2;
+  if (!map_heads(&qn, a.q_nope, a.n_q, a.n_heads, 128, pack, kRows / pack) ||
+      !map_heads(&qr, a.q_rope, a.n_q, a.n_heads, 64, pack, kRows / pack))
     return cudaErrorInvalidValue;
   if (a.n_k > 0) {
-    if (!map_heads(&kn, a.k_nope, a.n_k, a.n_kv_heads, 128, kKeys) ||
+    if (!map_heads(&kn, a.k_nope, a.n_k, a.n_kv_heads, 128, 1, kKeys) ||
         !map_rows(&kr, a.k_rope, a.k_rope_stride, a.n_k) ||
-        !map_heads(&v, a.v, a.n_k, a.n_kv_heads, 128, kKeys))
+        !map_heads(&v, a.v, a.n_k, a.n_kv_heads, 128, 1, kKeys))
       return cudaErrorInvalidValue;
   } else {
     kn = kr = v = qn;   // no key exists, so nothing is loaded through them
@@ -761,10 +767,11 @@ cudaError_t launch_prompt_attn(const PromptAttnArgs &a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // Heads are taken in groups whose keys and values stay in L2 together while
   // their blocks are worked off, most keys first within the group.
-  const long kv_bytes = 512L * a.n_k * a.n_kv_heads / a.n_heads + 1;   // of one query head
-  int group = a.n_heads;
-  while (group > 1 && (a.n_heads % group || kv_bytes * group > (60L << 20))) --group;
-  const long work = a.max_items * a.n_heads;
+  const int packs = a.n_heads / pack;
+  const long kv_bytes = 512L * a.n_k * a.n_kv_heads / packs + 1;   // of the heads of one pack
+  int group = packs;
+  while (group > 1 && (packs % group || kv_bytes * group > (60L << 20))) --group;
+  const long work = a.max_items * packs;
   const float scale_log2 = a.scale * 1.4426950408889634f;
   return launch_pdl(prompt_attn_kernel, dim3((unsigned)(work < sms ? work : sms)), dim3(kThreads),
                     kSmemBytes, s, qn, qr, kn, kr, v, a, scale_log2, group);

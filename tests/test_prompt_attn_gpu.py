@@ -42,10 +42,22 @@ def test_chunk_behind_cached_rows(n, m):
     go(dims_of(V2, 3, BF), [n], [m], 3, seed=n + m)
 
 
-@pytest.mark.parametrize("heads,kv", [(1, 1), (4, 1), (4, 2), (6, 2), (6, 3), (5, 5), (128, 128),
-                                      (128, 8), (256, 1)])
+@pytest.mark.parametrize("heads,kv", [(1, 1), (4, 1), (4, 2), (6, 2), (6, 3), (5, 5), (12, 1), (24, 2),
+                                      (128, 128), (128, 64), (128, 8), (128, 1), (256, 1)])
 def test_head_layouts(heads, kv):
     go(dims_of(V2, heads, BF), [70, 1, 190], [70, 150, 200], kv, seed=heads)
+
+
+@pytest.mark.parametrize("heads,kv", [(8, 1), (16, 1), (64, 1), (128, 1), (6, 1)])
+def test_single_tokens_of_grouped_heads(heads, kv):
+    """Short chunks of grouped heads behind long prefixes, and heads stored head by head."""
+    new, total = [1, 2, 1, 3, 17], [1000, 2, 81, 160, 700]
+    dims = dims_of(V2, heads, BF)
+    t, out, lse = go(dims, new, total, kv)
+    s = {k: (x.transpose(0, 1).contiguous().transpose(0, 1) if x.dim() == 3 else x)
+         for k, x in t.items()}
+    out2, lse2 = run_attn(dims, s, offsets(new), offsets(total))
+    assert torch.equal(out2, out) and torch.equal(lse2, lse)
 
 
 def test_packed_lengths_of_every_kind():
