@@ -55,7 +55,15 @@ struct PromptItem {
   int k0;    // first key of the sequence in the packed keys
   int lk;    // keys of the sequence
   int see;   // keys that the block's first token sees (may be <= 0); row r sees see + r
+  int part;  // -1, or the partial result that this range of the block's keys fills
 };
+
+// A block whose keys were cut into pieces: partial results first .. first + pieces - 1
+// (of every pack of heads) make up its rows.
+struct PromptJoin {
+  int q0, tokens, first, pieces;   // pieces == 0: nothing to join
+};
+
 
 // The attention kernel's work counter, and the CTAs that are through with it: the
 // last one sets both back to zero, which mla_workspace_init has them start at.
@@ -64,6 +72,9 @@ struct PromptPlanHeader {
   int next;
   unsigned done;
 };
+
+// Partial results of a call, one for each CTA at most.
+constexpr int kPromptParts = 148;
 
 struct PromptPlanArgs {
   const int32_t *cu_q, *cu_k;
@@ -99,6 +110,7 @@ __device__ __forceinline__ PromptItem prompt_item(int q0, int lq, int k0, int lk
   it.k0 = k0;
   it.lk = lk;
   it.see = r + lk - lq + 1;
+  it.part = -1;
   return it;
 }
 
@@ -119,6 +131,10 @@ struct PromptAttnArgs {
   const PromptItem *items;
   const int32_t *cu_q, *cu_k;
   int batch;
+  // Keys of few blocks cut into pieces (nullptr: no room, every block in one piece):
+  // [kPromptParts][256 rows][128], and the rows' m (log2 units) and l.
+  float *part_O, *part_m, *part_l;
+  PromptJoin *join;   // [max_items]
   void *out;   // [n_q][n_heads][d_v]
   float *lse;  // [n_q][n_heads] or nullptr
   int *err;

@@ -46,8 +46,31 @@ int least_tile_tokens(const mla_dims &d) {
 // mla_workspace_init clears); the plan's items follow.
 constexpr size_t kItemsAt = 256, kHeaderAt = 64;
 
+constexpr size_t kPartBytes = sizeof(float) * 256 * (128 + 2);   // O, m and l of a partial result
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Bytes up to the partial results, which follow where a call may need them.
+size_t plan_bytes(const mla_dims &d, int batch, int n_tokens) {
+  return align256(kItemsAt +
+                  sizeof(PromptItem) * (size_t)prompt_max_items(n_tokens, batch,
+                                                                least_tile_tokens(d)));
+}
+
+// Whether a grouping of the heads leaves fewer blocks than half the CTAs.
+bool few_blocks(const mla_dims &d, int batch, int n_tokens) {
+  if (d.dtype != MLA_BF16) return false;
+  for (int rep = 1; rep <= d.n_heads; ++rep)
+    if (d.n_heads % rep == 0 &&
+        2 * prompt_max_items(n_tokens, batch, tile_tokens(d, rep)) *
+                (d.n_heads >> pack_log2(rep)) <= kPromptParts)
+      return true;
+  return false;
+}
+
 size_t prompt_ws_bytes(const mla_dims &d, int batch, int n_tokens) {
-  return kItemsAt + sizeof(PromptItem) * (size_t)prompt_max_items(n_tokens, batch, least_tile_tokens(d));
+  return plan_bytes(d, batch, n_tokens) +
+         (few_blocks(d, batch, n_tokens) ? kPromptParts * kPartBytes : 0);
 }
 
 mla_status check_ws(const void *ws, size_t ws_bytes, size_t need) {
@@ -225,6 +248,12 @@ mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, in
   a.scale = api::softmax_scale(d);
   a.hdr = pa.hdr;
   a.items = pa.items;
+  if (few_blocks(d, batch, n_q)) {
+    a.part_O = reinterpret_cast<float *>(static_cast<char *>(ws) + plan_bytes(d, batch, n_q));
+    a.part_m = a.part_O + (size_t)kPromptParts * 256 * 128;
+    a.part_l = a.part_m + (size_t)kPromptParts * 256;
+    a.join = reinterpret_cast<PromptJoin *>(pa.items);   // the plan's place, which it does not use
+  }
   a.out = out;
   a.lse = lse;
   a.err = pa.err;

@@ -41,6 +41,8 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kRows = 128;              // query rows of a tile
 constexpr int kKeys = 80;               // keys of a step
+constexpr int kMinSteps = 4;            // of a piece of a block's keys
+constexpr int kSplitKeys = 1024;        // fewest keys of a call whose blocks are cut
 constexpr int kSched = 3;               // work items in flight between the warps
 constexpr int kWarpOut = 8;             // warps 8-11
 constexpr int kWarpLoad = 12, kWarpFix = 13, kWarpMma = 14, kWarps = 16;   // MMA: 14, 15
@@ -162,8 +164,14 @@ __device__ __forceinline__ int tile_steps(const PromptItem &it, int t, int lg) {
 // blocks that take longest start first.  A thread a sequence, then a thread an item;
 // the rank is counted (items^2 / 512 comparisons a thread).  A launch of its own
 // would cost about 6 us, this takes about 1.  Returns the number of items.
+//
+// split: there are fewer blocks than half the CTAs, so their keys are cut into as many
+// pieces as there are CTAs for, by their number of steps (at least kMinSteps a
+// piece).  A piece is an item of its own whose keys are a range of the block's; it
+// leaves an unnormalised result that the join kernel merges.
 // `scratch`: 4.2 KB of shared memory.
-__device__ __forceinline__ int own_plan(const PromptAttnArgs &a, PromptItem *list, int *scratch) {
+__device__ __forceinline__ int own_plan(const PromptAttnArgs &a, PromptItem *list, int *scratch,
+                                        bool split) {
   static_assert(kThreads == kPromptOwnItems, "a thread an item");
   int *first = scratch;          // [512] items before the sequence
   int *keys = first + 512;       // [512] of item i, before sorting
@@ -206,6 +214,41 @@ __device__ __forceinline__ int own_plan(const PromptAttnArgs &a, PromptItem *lis
   }
   keys[tid] = mine;
   __syncthreads();
+  if (split) {
+    // (items <= 74, so first[] has room behind them)
+    const int steps = (max(mine, 0) + kKeys - 1) / kKeys, packs = a.n_heads >> a.pack_log2;
+    int all = 0;
+    for (int i = 0; i < items; ++i) all += (keys[i] + kKeys - 1) / kKeys;
+    auto pieces = [&](int st) {
+      const int most = min(st / kMinSteps, (int)((long)st * kPromptParts / (max(all, 1) * packs)));
+      return max(1, most);
+    };
+    int at = 0, part = 0, n = 0;
+    for (int i = 0; i < items; ++i) {
+      const int c = pieces((keys[i] + kKeys - 1) / kKeys);
+      at += i < tid ? c : 0;
+      part += i < tid && c > 1 ? c : 0;
+      n += c;
+    }
+    if (tid < items) {
+      const int c = pieces(steps);
+      for (int i = 0; i < c; ++i) {
+        const int s0 = (int)((long)steps * i / c), s1 = (int)((long)steps * (i + 1) / c);
+        PromptItem x = it;
+        if (c > 1) {
+          x.k0 += s0 * kKeys;
+          x.lk = min(it.lk - s0 * kKeys, (s1 - s0) * kKeys);
+          x.see -= s0 * kKeys;
+          x.part = part + i;
+        }
+        list[at + i] = x;
+      }
+      if (blockIdx.x == 0) a.join[tid] = PromptJoin{it.q0, it.rows, part, c > 1 ? c : 0};
+    }
+    if (blockIdx.x == 0 && tid >= items && tid < a.max_items) a.join[tid] = PromptJoin{0, 0, 0, 0};
+    __syncthreads();
+    return n;
+  }
   if (tid < items) {
     int rank = 0;
     for (int i = 0; i < items; ++i) rank += keys[i] > mine || (keys[i] == mine && i < tid);
@@ -221,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tm_kn,
                        const __grid_constant__ CUtensorMap tm_kr,
                        const __grid_constant__ CUtensorMap tm_v, const PromptAttnArgs a,
-                       const float scale_log2, const int heads_per_group) {
+                       const float scale_log2, const int heads_per_group,
+                       const bool split) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars *bars = reinterpret_cast<Bars *>(smem + kOffBar);
   const Ctx ctx{bars, a.err};
@@ -279,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_launch();
   const bool own = a.max_items <= kPromptOwnItems;
   PromptItem *const own_items = reinterpret_cast<PromptItem *>(smem + kOffItems);
-  const int items = own ? own_plan(a, own_items, reinterpret_cast<int *>(smem + kOffOut))
+  const int items = own ? own_plan(a, own_items, reinterpret_cast<int *>(smem + kOffOut), split)
                         : a.hdr->items;
 
   // the k-th work item of this CTA, as a whole warp reads it
@@ -401,8 +445,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ni > 0) ok = wait_all(&bars->o_free[t], (ni - 1) & 1);
       if (!ok) break;
       ++ni;
-      inv_s[row] = see > 0 ? 1.f / l : 0.f;
-      inv_s[256 + row] = see > 0 ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+      if (w.it.part >= 0) {      // a piece of the row's keys: as they are
+        inv_s[row] = l;
+        inv_s[256 + row] = m;
+      } else {
+        inv_s[row] = see > 0 ? 1.f / l : 0.f;
+        inv_s[256 + row] = see > 0 ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->l_full[t]);
     }
@@ -413,6 +462,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float *inv_s = reinterpret_cast<const float *>(smem + kOffInv);
     uint8_t *stage = smem + kOffOut + (warp & 3) * 4096;   // [32 rows][8 units of 16 bytes]
     int no[2] = {0, 0};
+    // The tile's O, l and m for a piece of its keys, not normalised (32 columns at a
+    // time through the staging rows).
+    auto store_part = [&](const Work &w, int t, int steps, int toks, float l) {
+      const long slot = (long)w.it.part * (a.n_heads >> lg) + (w.head >> lg);
+      const long r0 = slot * 256 + 128 * t + warp_row;
+      if ((row >> lg) < toks) {
+        a.part_l[r0 + lane] = steps > 0 ? l : 0.f;
+        a.part_m[r0 + lane] = steps > 0 ? inv_s[256 + 128 * t + row] : -INFINITY;
+      }
+      if (steps == 0) return;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        float o[32];
+        tmem_ld32f(tmem + lane_off + kTmemO + 128 * t + 32 * q, o);
+        tmem_wait_ld();
+        if (q == 3) tc_fence_before();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4 *>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+              make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        __syncwarp();
+        if (q == 3 && lane == 0) mbar_arrive(&bars->o_free[t]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3), u = lane & 7;
+          const float4 x =
+              *reinterpret_cast<const float4 *>(stage + r * 128 + ((u ^ (r & 7)) << 4));
+          if (((warp_row + r) >> lg) < toks)
+            *reinterpret_cast<float4 *>(a.part_O + (r0 + r) * 128 + 32 * q + 4 * u) = x;
+        }
+        __syncwarp();
+      }
+    };
     bool ok = true;
     Work w;
     for (int k = 0; ok && take(k, w); ++k) {
@@ -431,6 +513,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++no[t];
           tc_fence_after();
           inv = inv_s[128 * t + row];
+        }
+        if (w.it.part >= 0) {
+          store_part(w, t, steps, toks, inv);
+          continue;
         }
         if ((row >> lg) < toks && a.lse)
           a.lse[at(row)] = steps > 0 ? inv_s[256 + 128 * t + row] : -INFINITY;
@@ -694,6 +780,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Rows whose keys were cut into pieces: M = max_j m_j, w_j = 2^(m_j - M),
+// out = sum_j w_j O_j / sum_j w_j l_j, lse = ln 2 (M + log2 sum_j w_j l_j), pieces in
+// order.  One warp a row: a lane a piece for m and l, then a lane four columns of O.  A
+// piece that the row sees nothing of has l = 0 and is not read.
+__global__ void __launch_bounds__(256) prompt_join_kernel(const PromptAttnArgs a) {
+  const int lane = threadIdx.x & 31, lg = a.pack_log2;
+  const int packs = a.n_heads >> lg, item = blockIdx.x / packs, pack = blockIdx.x % packs;
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  grid_dep_wait();
+  grid_dep_launch();
+  const PromptJoin jn = a.join[item];
+  if (jn.pieces == 0 || row >= jn.tokens << lg) return;
+  const long at0 = ((long)jn.first * packs + pack) * 256 + row, step = (long)packs * 256;
+  constexpr int kRounds = (kPromptParts + 31) / 32;
+  float lj[kRounds], mj[kRounds], top = -INFINITY;
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int j = 32 * r + lane;
+    lj[r] = j < jn.pieces ? a.part_l[at0 + j * step] : 0.f;
+    mj[r] = j < jn.pieces ? a.part_m[at0 + j * step] : 0.f;
+  }
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r)
+    if (lj[r] != 0.f) top = max3_nan(top, mj[r], top);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = max3_nan(top, __shfl_xor_sync(0xffffffffu, top, o), top);
+  float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const float w = lj[r] != 0.f ? ex2(mj[r] - top) : 0.f;
+    l += w * lj[r];
+    const int n = min(32, jn.pieces - 32 * r);
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (wj != 0.f)
+        x = *reinterpret_cast<const float4 *>(a.part_O + (at0 + (32 * r + j) * step) * 128 +
+                                              4 * lane);
+      acc[0] = fmaf(wj, x.x, acc[0]);
+      acc[1] = fmaf(wj, x.y, acc[1]);
+      acc[2] = fmaf(wj, x.z, acc[2]);
+      acc[3] = fmaf(wj, x.w, acc[3]);
+    }
+  }
+  l = warp_sum(l);
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  const long dst = (long)(jn.q0 + (row >> lg)) * a.n_heads + (pack << lg) + (row & ((1 << lg) - 1));
+  *reinterpret_cast<uint2 *>(static_cast<bf16 *>(a.out) + dst * 128 + 4 * lane) =
+      make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
+  if (a.lse && lane == 0) a.lse[dst] = l != 0.f ? (top + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
 // ------------------------------------------------------------------ host side
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -772,9 +911,15 @@ cudaError_t launch_prompt_attn(const PromptAttnArgs &a, cudaStream_t s) {
   int group = packs;
   while (group > 1 && (packs % group || kv_bytes * group > (60L << 20))) --group;
   const long work = a.max_items * packs;
+  // Few blocks with long keys: see own_plan.  (The bounds that the host knows decide;
+  // what the lengths then allow is decided on the device.)
+  const bool split = a.part_O && 2 * work <= sms && a.n_k >= kSplitKeys;
   const float scale_log2 = a.scale * 1.4426950408889634f;
-  return launch_pdl(prompt_attn_kernel, dim3((unsigned)(work < sms ? work : sms)), dim3(kThreads),
-                    kSmemBytes, s, qn, qr, kn, kr, v, a, scale_log2, group);
+  const long ctas = split ? (sms < kPromptParts ? sms : kPromptParts) : work < sms ? work : sms;
+  e = launch_pdl(prompt_attn_kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, s, qn, qr, kn,
+                 kr, v, a, scale_log2, split ? packs : group, split);
+  if (e != cudaSuccess || !split) return e;
+  return launch_pdl(prompt_join_kernel, dim3((unsigned)work, kPromptTileSm100 / 8), dim3(256), 0, s, a);
 }
 
 }  // namespace sm100

@@ -60,6 +60,69 @@ def test_single_tokens_of_grouped_heads(heads, kv):
     assert torch.equal(out2, out) and torch.equal(lse2, lse)
 
 
+@pytest.mark.parametrize("new,total,heads,kv", [
+    ([1], [9000], 1, 1), ([100], [3000], 2, 2), ([300, 1], [4000, 1], 4, 4),
+    ([1, 0, 5, 129], [2000, 700, 3, 129], 8, 8), ([2, 3], [1200, 20000], 16, 1),
+    ([700], [100], 1, 1), ([90, 33], [40, 3000], 3, 3), ([1, 1, 1], [1500, 0, 81], 128, 1),
+    ([17], [1023], 4, 4), ([17], [1024], 4, 4), ([9000], [9000], 1, 1)])
+def test_few_blocks_whose_keys_are_cut(new, total, heads, kv):
+    """Fewer blocks than half the multiprocessors: their keys are cut into pieces that are
+    merged, beside blocks of one piece, queries that see nothing and empty sequences."""
+    go(dims_of(V2, heads, BF), new, total, kv, seed=sum(total))
+
+
+def test_cut_keys_with_scores_far_apart():
+    go(dims_of(V2, 2, BF), [200], [5000], 2, spread=6.0)
+    dims = dims_of(V2, 2, BF)
+    t = attn_inputs(dims, 40, 4000, 2, 41)
+    t["q_nope"] = torch.ones_like(t["q_nope"])
+    ramp = torch.linspace(-40, 40, 4000, device="cuda")
+    t["k_nope"] = (ramp[:, None, None] / 10 + 0.1 * t["k_nope"].float()).to(BF)
+    out, lse = run_attn(dims, t, [0, 40], [0, 4000])
+    check_attn(dims, t, [0, 40], [0, 4000], out, lse)
+
+
+def test_cut_keys_outside_rows_and_bad_offsets():
+    dims = dims_of(V2, 2, BF)
+    cu_q, cu_k = [3, 20, 90], [100, 2100, 4000]
+    t = attn_inputs(dims, 100, 4100, 2, 43)
+    for name in ("k_nope", "k_rope", "v"):
+        t[name][:100] = math.nan
+        t[name][4000:] = math.inf
+    ws = workspace(dims, 2, 100)
+    out, lse = run_attn(dims, t, cu_q, cu_k, ws=ws)
+    check_attn(dims, t, cu_q, cu_k, out, lse)
+    for lo, hi in ((0, 3), (90, 100)):
+        assert (out[lo:hi] == 7).all() and (lse[lo:hi] == 7).all()
+    out2 = torch.full_like(out, 7.0)
+    L.mla_prompt_attn(dims, t["q_nope"], t["q_rope"], t["k_nope"], t["k_rope"], t["v"],
+                      i32([3, 20, 101]), i32(cu_k), out2, None, ws)
+    assert L.mla_get_device_error(ws) == 6
+    assert torch.equal(out2[:20], out[:20]) or (out2[20:] == 7).all()
+    assert (out2[20:] == 7).all()
+
+
+def test_cut_keys_give_the_same_bits_every_time():
+    dims = dims_of(V2, 4, BF)
+    t = attn_inputs(dims, 60, 6000, 4, 45)
+    cu_q, cu_k = i32([0, 60]), i32([0, 6000])
+    ws = workspace(dims, 1, 60)
+    outs = [torch.empty(60, 4, 128, dtype=BF, device="cuda") for _ in range(6)]
+    call = lambda o: L.mla_prompt_attn(dims, t["q_nope"], t["q_rope"], t["k_nope"],  # noqa: E731
+                                       t["k_rope"], t["v"], cu_q, cu_k, o, None, ws)
+    for o in outs[:5]:
+        call(o)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(outs[5])
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+
+
 def test_packed_lengths_of_every_kind():
     new = [0, 1, 128, 0, 129, 5, 700, 64, 256, 0]
     total = [0, 1, 128, 40, 129, 300, 700, 1000, 257, 0]
