@@ -258,8 +258,9 @@ size_t mla_prompt_workspace_size(const mla_dims *dims, int batch, int n_tokens);
  * and the row [c ; k_R], rounded once (int8 rows: quantised as described at
  * MLA_CACHE_INT8, from a c held in 64 bits), is written to slot p of sequence b.
  * With q_rope the same launch rotates the tokens' queries, q_out = RoPE_p(q_rope).
- * x: [n_tokens][d_c + d_rope], the projections W_DKV h and W_KR h, rows x_stride
- * elements apart (at least d_c + d_rope; MLA_BF16: a multiple of 8);
+ * x: [n_tokens][d_c + d_rope], the projections W_DKV h and W_KR h, of x_dtype:
+ * MLA_FP32 (products left unrounded, as mla_cache_append keeps them) or dims->dtype;
+ * rows x_stride elements apart (at least d_c + d_rope; MLA_BF16: a multiple of 8);
  * gamma: [d_c]; ctx_lens: [batch] rows that the sequences already have, or NULL
  * for none; q_rope, q_out: [n_tokens][n_heads][d_rope], both or neither (NULL);
  * q_out may be q_rope itself, but may not overlap it otherwise.
@@ -267,8 +268,8 @@ size_t mla_prompt_workspace_size(const mla_dims *dims, int batch, int n_tokens);
  * position has no page is not written and sets the error word (its queries are
  * rotated).  Two tokens of one call may not map to the same slot. */
 mla_status mla_prompt_append(const mla_dims *dims, const mla_paged_cache *cache, int batch,
-                             int n_tokens, const void *x, int64_t x_stride, const void *gamma,
-                             const int32_t *cu_tokens, const int32_t *ctx_lens,
+                             int n_tokens, const void *x, int x_dtype, int64_t x_stride,
+                             const void *gamma, const int32_t *cu_tokens, const int32_t *ctx_lens,
                              const mla_heads *q_rope, const mla_heads *q_out, void *ws,
                              size_t ws_bytes, mla_stream_t stream);
 

@@ -128,7 +128,7 @@ def lib() -> ctypes.CDLL:
         i64, ph = ctypes.c_int64, ctypes.POINTER(_Heads)
         L.mla_prompt_workspace_size.argtypes = [pd, i, i]
         L.mla_prompt_workspace_size.restype = sz
-        L.mla_prompt_append.argtypes = [pd, pc, i, i, vp, i64, vp, vp, vp, ph, ph, vp, sz, vp]
+        L.mla_prompt_append.argtypes = [pd, pc, i, i, vp, i, i64, vp, vp, vp, ph, ph, vp, sz, vp]
         L.mla_cache_gather.argtypes = [pd, pc, i, i, vp, vp, vp, vp, sz, vp]
         L.mla_prompt_attn.argtypes = [pd, i, i, i, i, ph, ph, ph, vp, i64, ph, vp, vp, vp, vp, vp,
                                       sz, vp]
@@ -322,13 +322,14 @@ def mla_prompt_append(dims: Dims, cache: PagedCache, x, gamma, cu_tokens, ctx_le
                       q_rope=None, q_out=None, ws: torch.Tensor = None, stream=None):
     """Packed rows into the paged cache, normalised and rotated, and the queries rotated.
 
-    x ``[tokens, d_c + d_rope]`` (any row stride), cu_tokens ``[batch + 1]`` int32,
+    x ``[tokens, d_c + d_rope]`` (any row stride; fp32 or the dims' type), cu_tokens ``[batch + 1]`` int32,
     ctx_lens ``[batch]`` int32 or None, q_rope and q_out ``[tokens, n_heads,
     d_rope]`` (any token and head strides; q_out may be q_rope) or None.
     """
     fn, dt, i32 = "mla_prompt_append", dims.torch_dtype, torch.int32
     dev, n, batch = _device(fn, x), x.shape[0], cu_tokens.numel() - 1
-    xp, xs = _rows(fn, dt, dev, x, "x", n, dims.d_c + dims.d_rope)
+    xd = x.dtype if x.dtype is torch.float32 else dt
+    xp, xs = _rows(fn, xd, dev, x, "x", n, dims.d_c + dims.d_rope)
     if (q_rope is None) != (q_out is None):
         raise ValueError(f"{fn}: q_rope and q_out go together")
     q = qo = None
@@ -336,7 +337,8 @@ def mla_prompt_append(dims: Dims, cache: PagedCache, x, gamma, cu_tokens, ctx_le
         q = ctypes.byref(_heads(fn, dt, dev, q_rope, "q_rope", n, dims.n_heads, dims.d_rope))
         qo = ctypes.byref(_heads(fn, dt, dev, q_out, "q_out", n, dims.n_heads, dims.d_rope))
     _launch(fn, lib().mla_prompt_append, dev, ws, stream, ctypes.byref(dims.c()),
-            ctypes.byref(_paged(fn, dims, dev, cache, batch)), batch, n, xp, xs,
+            ctypes.byref(_paged(fn, dims, dev, cache, batch)), batch, n, xp,
+            MLA_FP32 if xd is torch.float32 else MLA_BF16, xs,
             _dense(fn, dt, dev, gamma, "gamma", (dims.d_c,)),
             _dense(fn, i32, dev, cu_tokens, "cu_tokens", (batch + 1,)),
             None if ctx_lens is None else _dense(fn, i32, dev, ctx_lens, "ctx_lens", (batch,)),

@@ -20,6 +20,7 @@ struct HeadsView {
 struct PromptAppendArgs {
   const void *x;  // [n_tokens][d_c + d_rope], rows x_stride elements apart
   int64_t x_stride;
+  bool x_f32;     // x is fp32 (always with fp32 dims)
   const void *gamma;
   const int32_t *cu, *ctx;  // ctx == nullptr: all zero
   int batch, n_tokens, n_heads, d_c;

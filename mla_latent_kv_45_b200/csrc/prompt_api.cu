@@ -112,7 +112,8 @@ size_t mla_prompt_workspace_size(const mla_dims *dims, int batch, int n_tokens) 
 }
 
 mla_status mla_prompt_append(const mla_dims *dims, const mla_paged_cache *cache, int batch,
-                             int n_tokens, const void *x, int64_t x_stride, const void *gamma,
+                             int n_tokens, const void *x, int x_dtype, int64_t x_stride,
+                             const void *gamma,
                              const int32_t *cu_tokens, const int32_t *ctx_lens,
                              const mla_heads *q_rope, const mla_heads *q_out, void *ws,
                              size_t ws_bytes, mla_stream_t stream) {
@@ -121,6 +122,7 @@ mla_status mla_prompt_append(const mla_dims *dims, const mla_paged_cache *cache,
   const mla_dims &d = *dims;
   if (batch < 1 || n_tokens < 0 || !gamma || !cu_tokens || !q_rope != !q_out)
     return MLA_ERR_INVALID_ARG;
+  if (x_dtype != MLA_FP32 && x_dtype != d.dtype) return MLA_ERR_INVALID_ARG;
   MLA_TRY(check_ws(ws, ws_bytes, kItemsAt));
   if (!aligned16(gamma) || !aligned4(cu_tokens) || !aligned4(ctx_lens)) return MLA_ERR_ALIGNMENT;
   if (n_tokens == 0) return MLA_OK;
@@ -134,6 +136,7 @@ mla_status mla_prompt_append(const mla_dims *dims, const mla_paged_cache *cache,
   PromptAppendArgs a{};
   a.x = x;
   a.x_stride = x_stride;
+  a.x_f32 = x_dtype == MLA_FP32;
   a.gamma = gamma;
   a.cu = cu_tokens;
   a.ctx = ctx_lens;

@@ -61,6 +61,28 @@ __device__ __forceinline__ uint4 pack8(const float *f) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 8 values as loaded, turned into floats where they are needed.
+template <class X>
+struct Raw8;
+template <>
+struct Raw8<bf16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const bf16 *p) { v = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void get(float *f) const { unpack8(v, f); }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = reinterpret_cast<const float4 *>(p)[0];
+    b = reinterpret_cast<const float4 *>(p)[1];
+  }
+  __device__ __forceinline__ void get(float *f) const {
+    reinterpret_cast<float4 *>(f)[0] = a;
+    reinterpret_cast<float4 *>(f)[1] = b;
+  }
+};
+
 // ---------------------------------------------------------------------------
 // Cache append of packed rows
 // ---------------------------------------------------------------------------
@@ -137,7 +159,7 @@ constexpr int kSlab = 32;  // heads a warp rotates per round: 4 units of 8 pairs
 // A unit is 8 rotation pairs = two 16-byte vectors of a 64-wide head:
 // interleaved pairs (vectors 2u, 2u + 1) or split halves (vectors u, u + 4).  Lane l
 // handles unit l % 4, so its 8 cosines and sines stay in registers for all heads.
-template <bool kI8>
+template <bool kI8, class X>
 __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ RopeParams rp,
                                    int group) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -160,16 +182,15 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
       }
     }
   };
-  uint4 xc[2], xr[2];
+  Raw8<X> rc[2], rr[2];
   if (role < group - 1) {
     load(role * kSlab);
   } else {
-    const uint4 *x =
-        reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(a.x) + t * a.x_stride);
-    xc[0] = x[lane];
-    xc[1] = x[32 + lane];
-    xr[0] = x[64 + v0];
-    xr[1] = x[64 + v1];
+    const X *x = static_cast<const X *>(a.x) + t * a.x_stride;
+    rc[0].load(x + 8 * lane);
+    rc[1].load(x + 256 + 8 * lane);
+    rr[0].load(x + 512 + 8 * v0);
+    rr[1].load(x + 512 + 8 * v1);
   }
   const int b = warp_find_seq(a.cu, a.batch, t);
   if (b < 0) {
@@ -189,10 +210,7 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
     cs[i] = __shfl_sync(0xffffffffu, cf, 8 * u + i);
     sn[i] = __shfl_sync(0xffffffffu, sf, 8 * u + i);
   }
-  auto turn = [&](uint4 &p, uint4 &r) {
-    float f[16];
-    unpack8(p, f);
-    unpack8(r, f + 8);
+  auto turn = [&](float (&f)[16]) {     // the unit's two vectors
     if (rp.half) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) rope_rotate(cs[i], sn[i], f[i], f[8 + i]);
@@ -200,8 +218,6 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
 #pragma unroll
       for (int i = 0; i < 8; ++i) rope_rotate(cs[i], sn[i], f[2 * i], f[2 * i + 1]);
     }
-    p = pack8(f);
-    r = pack8(f + 8);
   };
 
   if (role < group - 1) {
@@ -211,10 +227,13 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
       for (int k = 0; k < 4; ++k) {
         const int h = h0 + 8 * k + (lane >> 2);
         if (h < a.n_heads) {
-          turn(p[k], r[k]);
+          float f[16];
+          unpack8(p[k], f);
+          unpack8(r[k], f + 8);
+          turn(f);
           uint4 *dst = reinterpret_cast<uint4 *>(qo + h * a.q_out.head);
-          dst[v0] = p[k];
-          dst[v1] = r[k];
+          dst[v0] = pack8(f);
+          dst[v1] = pack8(f + 8);
         }
       }
       h0 += (group - 1) * kSlab;
@@ -231,13 +250,15 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
     return;
   }
   const uint4 *g = static_cast<const uint4 *>(a.gamma);
-  float c[16], gm[16];
-  unpack8(xc[0], c);
-  unpack8(xc[1], c + 8);
+  float c[16], gm[16], xr[16];
+  rc[0].get(c);
+  rc[1].get(c + 8);
+  rr[0].get(xr);
+  rr[1].get(xr + 8);
   unpack8(g[lane], gm);
   unpack8(g[32 + lane], gm + 8);
-  uint4 kp = xr[0], kr = xr[1];
-  turn(kp, kr);
+  turn(xr);
+  const uint4 kp = pack8(xr), kr = pack8(xr + 8);
   const long slot = (long)page * a.page_size + pos % a.page_size;
   if (!kI8) {
     float ss = 0.f;
@@ -586,8 +607,12 @@ cudaError_t launch_prompt_append_bf16(const PromptAppendArgs &a, const RopeParam
   }
   const int per = group >= 8 ? 1 : 8 / group;
   const dim3 grid((a.n_tokens + per - 1) / per), block(32 * per * group);
-  return int8_rows ? launch_pdl(prompt_append_bf16<true>, grid, block, 0, s, a, rp, group)
-                   : launch_pdl(prompt_append_bf16<false>, grid, block, 0, s, a, rp, group);
+  if (a.x_f32)
+    return int8_rows
+               ? launch_pdl(prompt_append_bf16<true, float>, grid, block, 0, s, a, rp, group)
+               : launch_pdl(prompt_append_bf16<false, float>, grid, block, 0, s, a, rp, group);
+  return int8_rows ? launch_pdl(prompt_append_bf16<true, bf16>, grid, block, 0, s, a, rp, group)
+                   : launch_pdl(prompt_append_bf16<false, bf16>, grid, block, 0, s, a, rp, group);
 }
 
 cudaError_t launch_gather_f32(const GatherArgs &a, int row, cudaStream_t s) {

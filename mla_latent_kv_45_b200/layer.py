@@ -1,9 +1,13 @@
-"""One decode step of an MLA layer through the four C-ABI calls.
+"""An MLA layer through the C-ABI calls: one decode step, or a chunk of a prompt.
 
 The order is the pages' per-token inference flow ("解耦 RoPE（MLA 下）" §五):
 append the new token's [c ; k_R] row, build the absorbed query, attend over
 the whole cache (the new row included), then up-project.  Device tensors only;
 every step runs in the CUDA library.
+
+A prompt takes many tokens of several sequences at once and attends in the
+expanded form ("解耦 RoPE（MLA 下）" §七 ``forward_naive``), where the weights are
+plain matrix products of torch around the library's calls.
 """
 
 from __future__ import annotations
@@ -98,6 +102,86 @@ class DecodeLayer:
         st = L.mla_get_device_error(self.ws_append, self.side)
         st2 = L.mla_get_device_error(self.ws)
         return st if st != 0 else st2
+
+
+class PromptLayer:
+    """A chunk of new tokens of several sequences through one layer.
+
+    Weights as for ``DecodeLayer``; buffers for ``tokens`` new tokens of ``batch``
+    sequences that have ``rows`` cached rows in all once the chunk is appended.
+    Prompts may come in one chunk or in several: a chunk attends over everything its
+    sequences have in the cache.  The same cache then serves ``DecodeLayer``.
+    """
+
+    def __init__(self, dims: L.Dims, weights: dict, batch: int, tokens: int, rows: int,
+                 device="cuda"):
+        nbytes = L.mla_prompt_workspace_size(dims, batch, tokens)
+        if nbytes == 0:
+            raise ValueError("unsupported dims for the workspace")
+        self.dims, self.batch, self.tokens, self.n_rows = dims, batch, tokens, rows
+        w, dt, H = weights, dims.torch_dtype, dims.n_heads
+        # [out, in] weights as the right-hand sides of the products; the two
+        # projections of the cache row become one
+        self.w_row = torch.cat([w["W_DKV"], w["W_KR"]]).T
+        self.w_dq = None if w.get("W_DQ") is None else w["W_DQ"].T
+        self.w_uq, self.w_qr = w["W_UQ"].T, w["W_QR"].T
+        self.w_uk, self.w_uv = w["W_UK"].T, w["W_UV"].T
+        self.w_o = None if w.get("W_O") is None else w["W_O"].T
+        self.gamma = w["gamma"]
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        L.mla_workspace_init(self.ws)
+        new = lambda *s: torch.empty(*s, dtype=dt, device=device)  # noqa: E731
+        # the projections of the cache row stay in fp32 until they are normalised and
+        # rotated, as in the decode step
+        self.x = torch.empty(tokens, dims.d_c + dims.d_rope, dtype=torch.float32, device=device)
+        self.c_q = None if self.w_dq is None else new(tokens, self.w_dq.shape[1])
+        self.q_nope, self.q_rope = new(tokens, H, dims.d_nope), new(tokens, H, dims.d_rope)
+        self.rows = new(rows, dims.d_c + dims.d_rope)
+        self.k_nope, self.v = new(rows, H, dims.d_nope), new(rows, H, dims.d_v)
+        self.o = new(tokens, H, dims.d_v)
+        self.lse = torch.empty(tokens, H, dtype=torch.float32, device=device)
+        self.out = (self.o.view(tokens, -1) if self.w_o is None
+                    else new(tokens, self.w_o.shape[1]))
+
+    def step(self, cache: L.PagedCache, h: torch.Tensor, cu_tokens: torch.Tensor,
+             ctx_lens: Optional[torch.Tensor], cu_rows: torch.Tensor, stream=None) -> torch.Tensor:
+        """The layer output of the tokens ``h`` ``[tokens, d_model]``.
+
+        Sequence b's new tokens are rows ``cu_tokens[b] .. cu_tokens[b+1]`` of h and
+        follow the ``ctx_lens[b]`` rows (None: no rows) that it has in the cache;
+        ``cu_rows`` are the offsets of all its rows, cu_rows[b+1] - cu_rows[b] =
+        ctx_lens[b] + cu_tokens[b+1] - cu_tokens[b] (int32 device tensors, all read
+        on the device).  cache.seq_lens is not read.
+        """
+        s = stream if stream is not None else torch.cuda.current_stream(self.ws.device)
+        d = self.dims
+        with torch.cuda.stream(s):
+            torch.mm(h, self.w_row, out_dtype=torch.float32, out=self.x)
+            c_q = h if self.c_q is None else torch.mm(h, self.w_dq, out=self.c_q)
+            torch.mm(c_q, self.w_uq, out=self.q_nope.view(self.tokens, -1))
+            torch.mm(c_q, self.w_qr, out=self.q_rope.view(self.tokens, -1))
+            L.mla_prompt_append(d, cache, self.x, self.gamma, cu_tokens, ctx_lens, self.q_rope,
+                                self.q_rope, self.ws, s)
+            L.mla_cache_gather(d, cache, cu_rows, None, self.rows, self.ws, s)
+            c = self.rows[:, :d.d_c]
+            torch.mm(c, self.w_uk, out=self.k_nope.view(self.n_rows, -1))
+            torch.mm(c, self.w_uv, out=self.v.view(self.n_rows, -1))
+            L.mla_prompt_attn(d, self.q_nope, self.q_rope, self.k_nope, self.rows[:, d.d_c:],
+                              self.v, cu_tokens, cu_rows, self.o, self.lse, self.ws, s)
+            if self.w_o is not None:
+                torch.mm(self.o.view(self.tokens, -1), self.w_o, out=self.out)
+        return self.out
+
+    def capture(self, cache: L.PagedCache, h: torch.Tensor, cu_tokens: torch.Tensor,
+                ctx_lens: Optional[torch.Tensor], cu_rows: torch.Tensor) -> "StepGraph":
+        """The chunk over these buffers as a CUDA graph; lengths are read at replay."""
+        self.step(cache, h, cu_tokens, ctx_lens, cu_rows)
+        torch.cuda.synchronize()
+        return StepGraph(lambda s: self.step(cache, h, cu_tokens, ctx_lens, cu_rows, s), self.out)
+
+    def device_error(self) -> int:
+        """Synchronises; returns the device status of the workspace."""
+        return L.mla_get_device_error(self.ws)
 
 
 class StepGraph:

@@ -123,6 +123,26 @@ def test_append_and_gather_with_other_pages_and_wide_rows(page):
     assert torch.equal(rows, want)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("layout", [INTER, HALF])
+def test_append_of_fp32_projections(kind, layout):
+    """Products left in fp32: normalised and rotated before the one rounding."""
+    dims = dims_of(V2, 3, BF, 64, layout,
+                   L.MLA_CACHE_INT8 if kind == "int8" else L.MLA_CACHE_NATIVE)
+    new, ctx = [70, 0, 3], [5, 1, 200]
+    cu = offsets(new)
+    cache = paged(dims, [a + b for a, b in zip(new, ctx)], 33)
+    before = cache.pool.clone()
+    _, gamma, q = inputs(dims, cu[-1], 35)
+    g = torch.Generator(device="cuda").manual_seed(36)
+    wide = 1.4 * torch.randn(cu[-1], 600, generator=g, device="cuda")
+    x = wide[:, 16:592]
+    ws = workspace(dims, 3, cu[-1])
+    L.mla_prompt_append(dims, cache, x, gamma, i32(cu), i32(ctx), q, q, ws)
+    assert L.mla_get_device_error(ws) == 0
+    check_rows(dims, cache, before, new, ctx, x, gamma, cu)
+
+
 def test_append_of_zero_and_of_large_rows():
     """A row of zeros stays zero (code scale 1); values up to 1e30 normalise."""
     for fmt in (L.MLA_CACHE_NATIVE, L.MLA_CACHE_INT8):

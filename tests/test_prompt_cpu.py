@@ -25,14 +25,14 @@ def heads(ptr=A, token=128 * 64, head=64):
     return ctypes.byref(L._Heads(ptr, token, head))
 
 
-def append(lib, dims=V2, cache=None, batch=2, n=10, x=A, xs=576, gamma=A, cu=A, ctx=A, q="q",
+def append(lib, dims=V2, cache=None, batch=2, n=10, x=A, xd=0, xs=576, gamma=A, cu=A, ctx=A, q="q",
            qo="q", ws=A, wsb=BIG):
     d = dims.c()
     c = L._Cache(A, 8, A, 4, None) if cache is None else cache
     q = heads() if q == "q" else q
     qo = heads() if qo == "q" else qo
-    return lib.mla_prompt_append(ctypes.byref(d), ctypes.byref(c), batch, n, x, xs, gamma, cu, ctx,
-                                 q, qo, ws, wsb, None)
+    return lib.mla_prompt_append(ctypes.byref(d), ctypes.byref(c), batch, n, x, xd, xs, gamma,
+                                 cu, ctx, q, qo, ws, wsb, None)
 
 
 def gather(lib, dims=V2, cache=None, batch=2, n=10, cu=A, first=None, rows=A, ws=A, wsb=BIG):
@@ -67,7 +67,7 @@ def test_append_refusals(lib):
     assert append(lib, L.Dims(8, 512, 64, 128, 128, 0)) == ARG
     assert append(lib, L.Dims(4, 16, 8, 8, 8, 16, L.MLA_FP32, cache_format=1)) == SHAPE
     for bad in (dict(x=None), dict(gamma=None), dict(cu=None), dict(batch=0), dict(n=-1),
-                dict(xs=575), dict(xs=0), dict(ws=None), dict(q=None), dict(qo=None),
+                dict(xs=575), dict(xs=0), dict(xd=2), dict(xd=-1), dict(ws=None), dict(q=None), dict(qo=None),
                 dict(q=heads(None)), dict(q=heads(A, 8192, 63)), dict(qo=heads(A, 63, 64)),
                 dict(q=heads(A, 0, 64)), dict(qo=heads(A, 8192, -64)),
                 dict(cache=L._Cache(None, 8, A, 4, None)), dict(cache=L._Cache(A, 0, A, 4, None)),
@@ -78,6 +78,8 @@ def test_append_refusals(lib):
                 dict(q=heads(A, 8192 + 64, 66)), dict(cache=L._Cache(A + 8, 8, A, 4, None))):
         assert append(lib, **bad) == ALIGN, bad
     assert append(lib, wsb=100) == WS
+    assert append(lib, xd=1, wsb=100) == WS        # fp32 x beside bf16 rows
+    assert append(lib, TINY, xd=0) == ARG
     assert append(lib, n=0) == OK                  # nothing to do: no launch
 
 
