@@ -246,7 +246,8 @@ typedef struct {
 } mla_heads;
 
 /* Bytes of workspace the prompt calls need for `batch` sequences of n_tokens
- * new tokens in all.  Initialise it with mla_workspace_init; device errors are
+ * new tokens in all (grows with both, so the largest call's does for all of them).
+ * Initialise it with mla_workspace_init before its first use; device errors are
  * read with mla_get_device_error.  Calls that may overlap (other streams, graphs
  * that are replayed at the same time) need a workspace each. */
 size_t mla_prompt_workspace_size(const mla_dims *dims, int batch, int n_tokens);
@@ -300,8 +301,9 @@ mla_status mla_cache_gather(const mla_dims *dims, const mla_paged_cache *cache, 
  * may be NULL when n_k is 0.  With MLA_BF16 the weights of a softmax are rounded
  * to bf16 for the product with v (their sum is not); scores, maxima, sums and
  * the accumulator are fp32.  Keys and values outside their own sequence never
- * reach a result, whatever they hold; within a sequence an infinite or NaN v_j
- * may make rows of its 128-key tile that come before it NaN as well.
+ * reach a result, whatever they hold; within a sequence a score that a query does
+ * not see never does, but an infinite or NaN v_j may reach queries that come up to
+ * 206 tokens before it as well (MLA_BF16: a masked weight is 0, and 0 * NaN is NaN).
  * A sequence whose offsets do not ascend or leave [0, n_q] or [0, n_k] is
  * skipped (its rows of out and lse keep what they held) and sets the error word. */
 mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, int n_kv_heads,

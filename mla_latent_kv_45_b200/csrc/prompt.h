@@ -132,8 +132,8 @@ struct PromptAttnArgs {
   const PromptItem *items;
   const int32_t *cu_q, *cu_k;
   int batch;
-  // Keys of few blocks cut into pieces (nullptr: no room, every block in one piece):
-  // [kPromptParts][256 rows][128], and the rows' m (log2 units) and l.
+  // Keys of few blocks cut into pieces: [kPromptParts][256 rows][128], and the rows'
+  // m (log2 units) and l.
   float *part_O, *part_m, *part_l;
   PromptJoin *join;   // [max_items]
   void *out;   // [n_q][n_heads][d_v]

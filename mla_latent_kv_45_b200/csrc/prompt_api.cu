@@ -50,27 +50,16 @@ constexpr size_t kPartBytes = sizeof(float) * 256 * (128 + 2);   // O, m and l o
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Bytes up to the partial results, which follow where a call may need them.
+// Bytes up to the partial results (20 MB, bf16), which small calls over long keys use.
+// They are always part of the size, so that a workspace for many tokens does for few.
 size_t plan_bytes(const mla_dims &d, int batch, int n_tokens) {
   return align256(kItemsAt +
                   sizeof(PromptItem) * (size_t)prompt_max_items(n_tokens, batch,
                                                                 least_tile_tokens(d)));
 }
 
-// Whether a grouping of the heads leaves fewer blocks than half the CTAs.
-bool few_blocks(const mla_dims &d, int batch, int n_tokens) {
-  if (d.dtype != MLA_BF16) return false;
-  for (int rep = 1; rep <= d.n_heads; ++rep)
-    if (d.n_heads % rep == 0 &&
-        2 * prompt_max_items(n_tokens, batch, tile_tokens(d, rep)) *
-                (d.n_heads >> pack_log2(rep)) <= kPromptParts)
-      return true;
-  return false;
-}
-
 size_t prompt_ws_bytes(const mla_dims &d, int batch, int n_tokens) {
-  return plan_bytes(d, batch, n_tokens) +
-         (few_blocks(d, batch, n_tokens) ? kPromptParts * kPartBytes : 0);
+  return plan_bytes(d, batch, n_tokens) + (d.dtype == MLA_BF16 ? kPromptParts * kPartBytes : 0);
 }
 
 mla_status check_ws(const void *ws, size_t ws_bytes, size_t need) {
@@ -251,7 +240,7 @@ mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, in
   a.scale = api::softmax_scale(d);
   a.hdr = pa.hdr;
   a.items = pa.items;
-  if (few_blocks(d, batch, n_q)) {
+  if (d.dtype == MLA_BF16) {
     a.part_O = reinterpret_cast<float *>(static_cast<char *>(ws) + plan_bytes(d, batch, n_q));
     a.part_m = a.part_O + (size_t)kPromptParts * 256 * 128;
     a.part_l = a.part_m + (size_t)kPromptParts * 256;

@@ -9,23 +9,34 @@
 // in shared memory.  A row is a (token, head) pair.  With one key head per query head
 // they are 256 tokens of one head; grouped heads are packed, 2^lg heads of the group
 // (the largest power of two that divides it, 128 at most) of 256 / 2^lg tokens, so a
-// key head is read once for all of them and short chunks still fill a tile.  Per step of 80 keys a tile costs
-// S = Q K^T (K = 192, the two score terms are one product) and O += P V.
+// key head is read once for all of them and short chunks still fill a tile (4 chunks
+// of 64 tokens over 2000 rows, 128 heads in 8 groups: 45 us, 113 us a head at a time).
+// Per step of 80 keys a tile costs S = Q K^T (K = 192, the two score terms are one
+// product) and O += P V.
 //  * 80 keys a step, because TMEM then holds S (80 columns) beside P (bf16, 40
 //    columns) and O (128) of both tiles: 496 of 512 columns.  A step's scores are
 //    computed as soon as the previous step's have been read into registers, and
-//    the products P V run while the next softmax does.
+//    the products P V run while the next softmax does.  (128 keys with P in the
+//    place of S: 2446 us for 8192 tokens and 128 heads, this 2253 us in the same run.)
 //  * Warps 0-3 and 4-7 are the softmax of tile 0 and 1, one thread a row: no
-//    reduction crosses threads.
+//    reduction crosses threads.  (Two threads a row: 10 % slower.)
 //  * m moves only when the maximum grows by more than 2^8 (p stays below
 //    256); only then does the thread rescale O.
 //  * Warps 8-11 write the output of an item through shared memory (whole rows
 //    of 128 bytes) while the others are at the next one; warp 12 loads Q, K and V
-//    by TMA (two stages each), warp 13 issues the MMAs, warp 14 zeroes values
-//    behind a sequence's last key.
+//    by TMA (two stages of keys and values); warp 13 zeroes values behind a
+//    sequence's last key; warps 14 and 15 issue the MMAs, one thread a tile (one
+//    thread for both was the bottleneck: every wait of one tile held up the other).
 //  * Work comes from a counter: the CTAs are persistent and fetch (block, head)
 //    pairs, blocks with most keys first.
 //  * Every wait is bounded as in the decode kernel; on expiry the error word is set.
+//
+// What bounds it: a step takes about 2180 cycles.  The MMAs read 196 KB of operands
+// from shared memory in it and TMA writes 50 KB there, which at 128 bytes a cycle is
+// 1920 cycles; the softmax of a tile is a chain of about 1830.  An item costs about
+// 6000 cycles beside its steps (the tile with the earlier rows waits for the other).
+// 8192 tokens, 128 heads: 2.01 ms by itself (1370 TFLOP/s, 84 % of the measured
+// matrix rate), 2.3 ms back to back, where the power limit lowers the clock.
 #include <cuda.h>
 
 #include "api_checks.h"
@@ -198,7 +209,7 @@ __device__ __forceinline__ int own_plan(const PromptAttnArgs &a, PromptItem *lis
     before += i < (tid >> 5) ? warp_tot[i] : 0;
     items += warp_tot[i];
   }
-  items = min(items, kPromptOwnItems);   // offsets that overlap could ask for more
+  items = min(items, (int)a.max_items);   // offsets that overlap could ask for more
   first[tid] = before + v - n;
   __syncthreads();
   PromptItem it{};
@@ -215,7 +226,7 @@ __device__ __forceinline__ int own_plan(const PromptAttnArgs &a, PromptItem *lis
   keys[tid] = mine;
   __syncthreads();
   if (split) {
-    // (items <= 74, so first[] has room behind them)
+    // (items <= max_items <= 74 and 148 pieces at most beside them fit the list)
     const int steps = (max(mine, 0) + kKeys - 1) / kKeys, packs = a.n_heads >> a.pack_log2;
     int all = 0;
     for (int i = 0; i < items; ++i) all += (keys[i] + kKeys - 1) / kKeys;
@@ -913,7 +924,7 @@ cudaError_t launch_prompt_attn(const PromptAttnArgs &a, cudaStream_t s) {
   const long work = a.max_items * packs;
   // Few blocks with long keys: see own_plan.  (The bounds that the host knows decide;
   // what the lengths then allow is decided on the device.)
-  const bool split = a.part_O && 2 * work <= sms && a.n_k >= kSplitKeys;
+  const bool split = 2 * work <= sms && 2 * work <= kPromptParts && a.n_k >= kSplitKeys;
   const float scale_log2 = a.scale * 1.4426950408889634f;
   const long ctas = split ? (sms < kPromptParts ? sms : kPromptParts) : work < sms ? work : sms;
   e = launch_pdl(prompt_attn_kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, s, qn, qr, kn,

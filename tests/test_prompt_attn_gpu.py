@@ -141,24 +141,35 @@ def test_more_sequences_than_a_block_plans_for_itself():
     go(dims_of(V2, 1, BF), new, total, 1)
 
 
-@pytest.mark.parametrize("batch", [3, 1200])
-def test_offsets_that_overlap(batch):
+@pytest.mark.parametrize("batch,n,heads", [(3, 300, 1), (1200, 300, 1), (60, 2000, 1),
+                                           (400, 2000, 2)])
+def test_offsets_that_overlap(batch, n, heads):
     """Descending offsets make sequences overlap: more blocks than the tokens have.  The error
-    word is set, nothing outside the tensors is touched, and the next call is right."""
-    dims = dims_of(V2, 1, BF)
-    t = attn_inputs(dims, 300, 300, 1, 31)
-    ws = workspace(dims, batch, 300)
-    guard = torch.full((4096,), 7, dtype=torch.uint8, device="cuda")
-    cu = [0, 300] * (batch // 2) + [0, 300][:batch % 2 + 1]
-    out = torch.empty(300, 1, 128, dtype=BF, device="cuda")
+    word is set, the workspace is not left, and the next call is right."""
+    dims = dims_of(V2, heads, BF)
+    t = attn_inputs(dims, n, n, heads, 31)
+    size = L.mla_prompt_workspace_size(dims, batch, n)
+    whole = torch.full((size + 65536,), 7, dtype=torch.uint8, device="cuda")
+    ws = whole[:size]
+    L.mla_workspace_init(ws)
+    cu = [0, n] * (batch // 2) + [0, n][:batch % 2 + 1]
+    out = torch.empty(n, heads, 128, dtype=BF, device="cuda")
     L.mla_prompt_attn(dims, t["q_nope"], t["q_rope"], t["k_nope"], t["k_rope"], t["v"], i32(cu),
                       i32(cu), out, None, ws)
     assert L.mla_get_device_error(ws) == 6
-    assert (guard == 7).all()
-    pad = [0] * batch + [300]
-    run_attn(dims, t, pad, pad, ws=ws)
-    out, lse = run_attn(dims, t, [0, 300], [0, 300])
-    check_attn(dims, t, [0, 300], [0, 300], out, lse)
+    assert (whole[size:] == 7).all()
+    pad = [0] * batch + [n]
+    out, lse = run_attn(dims, t, pad, pad, ws=ws)
+    check_attn(dims, t, pad, pad, out, lse)
+
+
+def test_a_workspace_for_many_tokens_does_for_few():
+    dims = dims_of(V2, 4, BF)
+    ws = workspace(dims, 64, 8192)
+    for new, total in (([1], [5000]), ([300, 2], [1500, 2]), ([1] * 64, [90] * 64)):
+        t = attn_inputs(dims, sum(new), sum(total), 1, 35)
+        out, lse = run_attn(dims, t, offsets(new), offsets(total), ws=ws)
+        check_attn(dims, t, offsets(new), offsets(total), out, lse)
 
 
 def test_refusals_on_the_device():

@@ -54,6 +54,9 @@ def attn(lib, dims=V2, batch=2, n_q=10, n_k=10, kv=128, qn=None, qr=None, kn=Non
 def test_workspace_size(lib):
     size = L.mla_prompt_workspace_size
     assert size(V2, 4, 0) > 0 and size(V2, 4, 100000) > size(V2, 4, 1000)
+    sizes = [size(L.Dims(16, 512, 64, 128, 128, 64), b, n) for b, n in
+             ((1, 1), (1, 100), (3, 100), (3, 3001), (70, 3001), (70, 90000))]
+    assert sizes == sorted(sizes)
     assert size(V2, 0, 10) == 0 and size(V2, 1, -1) == 0
     assert size(L.Dims(257, 512, 64, 128, 128, 64), 1, 1) == 0
     assert size(L.Dims(16, 512, 64, 128, 128, 1), 1, 1) > 0
