@@ -2,7 +2,7 @@
 
 The compute lives in ``libmla_b200.so`` (C ABI in ``include/mla.h``); this
 package holds the ctypes binding (``_lib``), the in-tree build script
-(``build``), a decode-step driver over the four calls (``layer``) and the seeded
+(``build``), drivers of a decode step and of a prompt over the calls (``layer``) and the seeded
 input generator (``synth``).
 """
 
