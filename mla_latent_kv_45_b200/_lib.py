@@ -76,10 +76,19 @@ class Dims:
     softmax_scale: float = 0.0
     cache_format: int = MLA_CACHE_NATIVE
 
+    def __setattr__(self, name, value):
+        self.__dict__.pop("_c", None)
+        self.__dict__[name] = value
+
     def c(self) -> _Dims:
-        return _Dims(self.n_heads, self.d_c, self.d_rope, self.d_nope, self.d_v, self.page_size,
-                     self.dtype, self.rope_layout, self.rope_base, self.rms_eps,
-                     self.softmax_scale, self.cache_format)
+        """The C struct (made once; setting a field drops it)."""
+        c = self.__dict__.get("_c")
+        if c is None:
+            c = _Dims(self.n_heads, self.d_c, self.d_rope, self.d_nope, self.d_v, self.page_size,
+                      self.dtype, self.rope_layout, self.rope_base, self.rms_eps,
+                      self.softmax_scale, self.cache_format)
+            self.__dict__["_c"] = c
+        return c
 
     @property
     def torch_dtype(self):
@@ -293,22 +302,24 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _launch(fn: str, call, dev: int, ws: torch.Tensor, stream, *args):
-    """Calls the library on `stream` (default: the tensors' device's current one), with the
-    tensors' device current."""
+def _on(fn: str, dev: int, ws: torch.Tensor, stream) -> int:
+    """The stream to launch on (default: the device's current one), after a look at ws."""
     if ws is None or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"{fn}: ws is not a contiguous tensor on cuda:{dev}")
     if stream is None:
-        handle = _raw_stream(dev)
-    elif stream.device_index != dev:
+        return _raw_stream(dev)
+    if stream.device_index != dev:
         raise ValueError(f"{fn}: stream on {stream.device}, tensors on cuda:{dev}")
-    else:
-        handle = stream.cuda_stream
+    return stream.cuda_stream
+
+
+def _call(fn: str, dev: int, call, *args):
+    """Calls the library with the tensors' device current."""
     if torch.cuda.current_device() == dev:
-        st = call(*args, ws.data_ptr(), ws.nbytes, handle)
+        st = call(*args)
     else:
         with torch.cuda.device(dev):
-            st = call(*args, ws.data_ptr(), ws.nbytes, handle)
+            st = call(*args)
     if st != 0:
         raise MlaError(fn, st)
 
@@ -336,13 +347,14 @@ def mla_prompt_append(dims: Dims, cache: PagedCache, x, gamma, cu_tokens, ctx_le
     if q_rope is not None:
         q = ctypes.byref(_heads(fn, dt, dev, q_rope, "q_rope", n, dims.n_heads, dims.d_rope))
         qo = ctypes.byref(_heads(fn, dt, dev, q_out, "q_out", n, dims.n_heads, dims.d_rope))
-    _launch(fn, lib().mla_prompt_append, dev, ws, stream, ctypes.byref(dims.c()),
+    handle = _on(fn, dev, ws, stream)
+    _call(fn, dev, lib().mla_prompt_append, ctypes.byref(dims.c()),
             ctypes.byref(_paged(fn, dims, dev, cache, batch)), batch, n, xp,
             MLA_FP32 if xd is torch.float32 else MLA_BF16, xs,
             _dense(fn, dt, dev, gamma, "gamma", (dims.d_c,)),
             _dense(fn, i32, dev, cu_tokens, "cu_tokens", (batch + 1,)),
             None if ctx_lens is None else _dense(fn, i32, dev, ctx_lens, "ctx_lens", (batch,)),
-            q, qo)
+            q, qo, ws.data_ptr(), ws.nbytes, handle)
 
 
 def mla_cache_gather(dims: Dims, cache: PagedCache, cu_rows, first_rows, rows,
@@ -351,11 +363,13 @@ def mla_cache_gather(dims: Dims, cache: PagedCache, cu_rows, first_rows, rows,
     packed at cu_rows ``[batch + 1]``; int8 rows come back as the values they hold."""
     fn, i32 = "mla_cache_gather", torch.int32
     dev, n, batch = _device(fn, rows), rows.shape[0], cu_rows.numel() - 1
-    _launch(fn, lib().mla_cache_gather, dev, ws, stream, ctypes.byref(dims.c()),
+    handle = _on(fn, dev, ws, stream)
+    _call(fn, dev, lib().mla_cache_gather, ctypes.byref(dims.c()),
             ctypes.byref(_paged(fn, dims, dev, cache, batch)), batch, n,
             _dense(fn, i32, dev, cu_rows, "cu_rows", (batch + 1,)),
             None if first_rows is None else _dense(fn, i32, dev, first_rows, "first_rows", (batch,)),
-            _dense(fn, dims.torch_dtype, dev, rows, "rows", (n, dims.d_c + dims.d_rope)))
+            _dense(fn, dims.torch_dtype, dev, rows, "rows", (n, dims.d_c + dims.d_rope)),
+            ws.data_ptr(), ws.nbytes, handle)
 
 
 def mla_prompt_attn(dims: Dims, q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, out, lse=None,
@@ -372,7 +386,8 @@ def mla_prompt_attn(dims: Dims, q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, o
     dev, n_q, n_k, off = _device(fn, q_nope), q_nope.shape[0], k_nope.shape[0], cu_q.shape
     n_kv = k_nope.shape[1]
     krp, krs = _rows(fn, dt, dev, k_rope, "k_rope", n_k, dims.d_rope)
-    _launch(fn, lib().mla_prompt_attn, dev, ws, stream, ctypes.byref(dims.c()), off[0] - 1, n_q,
+    handle = _on(fn, dev, ws, stream)
+    _call(fn, dev, lib().mla_prompt_attn, ctypes.byref(dims.c()), off[0] - 1, n_q,
             n_k, n_kv, ctypes.byref(_heads(fn, dt, dev, q_nope, "q_nope", n_q, H, dims.d_nope)),
             ctypes.byref(_heads(fn, dt, dev, q_rope, "q_rope", n_q, H, dims.d_rope)),
             ctypes.byref(_heads(fn, dt, dev, k_nope, "k_nope", n_k, n_kv, dims.d_nope)), krp, krs,
@@ -380,7 +395,8 @@ def mla_prompt_attn(dims: Dims, q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, o
             _dense(fn, i32, dev, cu_q, "cu_q", (off[0],)),
             _dense(fn, i32, dev, cu_k, "cu_k", (off[0],)),
             _dense(fn, dt, dev, out, "out", (n_q, H, dims.d_v)),
-            None if lse is None else _dense(fn, torch.float32, dev, lse, "lse", (n_q, H)))
+            None if lse is None else _dense(fn, torch.float32, dev, lse, "lse", (n_q, H)),
+            ws.data_ptr(), ws.nbytes, handle)
 
 
 def mla_noalloc_get_device_error(stream=None) -> int:
