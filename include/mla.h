@@ -248,8 +248,9 @@ typedef struct {
 /* Bytes of workspace the prompt calls need for `batch` sequences of n_tokens
  * new tokens in all (grows with both, so the largest call's does for all of them).
  * Initialise it with mla_workspace_init before its first use; device errors are
- * read with mla_get_device_error.  Calls that may overlap (other streams, graphs
- * that are replayed at the same time) need a workspace each. */
+ * read with mla_get_device_error.  It may serve the other calls as well, as far as
+ * its size does.  Calls that may overlap (other streams, graphs that are replayed
+ * at the same time) need a workspace each. */
 size_t mla_prompt_workspace_size(const mla_dims *dims, int batch, int n_tokens);
 
 /* Cache append of packed rows ("解耦 RoPE（MLA 下）" §五 steps 2-3 for every

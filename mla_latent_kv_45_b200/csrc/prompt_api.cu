@@ -43,8 +43,10 @@ int least_tile_tokens(const mla_dims &d) {
 }
 
 // The error word and the plan header share the first 256 bytes (the part that
-// mla_workspace_init clears); the plan's items follow.
-constexpr size_t kItemsAt = 256, kHeaderAt = 64;
+// mla_workspace_init clears); the plan's items follow.  The header holds counters that
+// outlive a call, so it lies where no other call of the library writes: a workspace
+// may serve decode and prompt calls in turn.
+constexpr size_t kItemsAt = 256, kHeaderAt = 192;
 
 constexpr size_t kPartBytes = sizeof(float) * 256 * (128 + 2);   // O, m and l of a partial result
 

@@ -163,6 +163,26 @@ def test_offsets_that_overlap(batch, n, heads):
     check_attn(dims, t, pad, pad, out, lse)
 
 
+def test_a_workspace_serves_decode_and_prompt_calls_in_turn():
+    dims = dims_of(V2, 128, BF)
+    size = max(L.mla_workspace_size(dims, 2, 512, 0, 0), L.mla_prompt_workspace_size(dims, 3, 400))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    L.mla_workspace_init(ws)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    pool = torch.randn(8, 64, 576, generator=g, device="cuda").to(BF)
+    cache = L.PagedCache(pool, i32([[0, 3, 5], [1, 2, 6]]), i32([150, 64]))
+    q_lat = torch.randn(2, 128, 576, generator=g, device="cuda").to(BF)
+    z = [torch.empty(2, 128, 512, dtype=BF, device="cuda") for _ in range(3)]
+    new, total = [300, 1, 90], [300, 200, 90]
+    t = attn_inputs(dims, sum(new), sum(total), 128, 37)
+    for i in range(3):
+        L.mla_decode_attn(dims, cache, q_lat, z[i], None, 0, ws)
+        assert L.mla_get_device_error(ws) == 0
+        out, lse = run_attn(dims, t, offsets(new), offsets(total), ws=ws)
+        check_attn(dims, t, offsets(new), offsets(total), out, lse)
+    assert torch.equal(z[0], z[1]) and torch.equal(z[0], z[2])
+
+
 def test_a_workspace_for_many_tokens_does_for_few():
     dims = dims_of(V2, 4, BF)
     ws = workspace(dims, 64, 8192)
