@@ -610,6 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kv = w.head / rep;
         const int n_t[2] = {tile_steps(w.it, 0, lg), tile_steps(w.it, 1, lg)};
         const int n = max(n_t[0], n_t[1]);
+        // no keys follow soon: the values of the step before may not wait for them
+        if (n == 0 && gv < gk) ok = load_v();
         // Q of tile t, once the item before has its last scores
         auto load_q = [&](int t) -> bool {
           if (n_t[t] == 0) return true;
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(dst, &tm_kn, 0, kv, tok, &bars->k_full[u]);
           tma_load_3d(dst + kKBox, &tm_kn, 64, kv, tok, &bars->k_full[u]);
           tma_load_2d(dst + 2 * kKBox, &tm_kr, 0, tok, &bars->k_full[u]);
-          if (g > 0) ok = load_v();
+          if (gv < g) ok = load_v();      // (of the step before, if not already on its way)
           v_tok = tok;
           v_kv = kv;
           v_left = w.it.lk - j * kKeys;
@@ -694,19 +696,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       int nw = 0;                           // items read
       int no = 0, ni = 0, ns = 0, np = 0;   // of the tile: Q tiles, items, scores, products
       int n_t = 0, n = 0;                   // the item's steps: of this tile, in all
-      // the next item that has any keys
+      // The next item.  One at a time: an item without keys may not hold up the product
+      // of the item before, which the output warps need before they take more items.
       auto next_work = [&]() -> bool {
-        while (true) {
-          const int slot = nw % kSched;
-          if (!wait_bar(ctx, &bars->w_full[slot], (nw / kSched) & 1)) return false;
-          ++nw;
-          const Work w = bars->work[slot];
-          mbar_arrive(&bars->w_empty[slot]);
-          if (w.head < 0) return false;
-          n_t = tile_steps(w.it, t, lg);
-          n = max(n_t, tile_steps(w.it, t ^ 1, lg));
-          if (n > 0) return true;
-        }
+        const int slot = nw % kSched;
+        if (!wait_bar(ctx, &bars->w_full[slot], (nw / kSched) & 1)) return false;
+        ++nw;
+        const Work w = bars->work[slot];
+        mbar_arrive(&bars->w_empty[slot]);
+        if (w.head < 0) return false;
+        n_t = tile_steps(w.it, t, lg);
+        n = max(n_t, tile_steps(w.it, t ^ 1, lg));
+        return true;
       };
       // S = Q K^T with the keys of step g, once the scores before have been read
       auto scores = [&](int g, bool first, bool last) -> bool {
@@ -754,6 +755,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool more = next_work(), ok = true, ahead = false;   // ahead: the item's first S is out
       for (int g0 = 0; more && ok;) {
         const int steps = n_t, all = n;
+        if (all == 0) {
+          more = next_work();
+          continue;
+        }
         if (steps > 0 && !ahead) ok = scores(g0, true, steps == 1);
         ahead = false;
         for (int j = 0; j < steps && ok; ++j) {

@@ -213,6 +213,19 @@ def test_refusals_on_the_device():
     assert e.value.status == 4
 
 
+@pytest.mark.parametrize("batch,heads", [(200, 8), (700, 3), (40, 128)])
+def test_many_sequences_without_keys(batch, heads):
+    """Queries of many sequences without a key, behind and between sequences that have keys:
+    a block without keys may not hold up the block before it."""
+    new = [1 + (7 * i) % 30 for i in range(batch)]
+    total = [0 if i % 5 else n + i % 90 for i, n in enumerate(new)]
+    go(dims_of(V2, heads, BF), new, total, heads)
+    go(dims_of(V2, heads, BF), new + [600], [0] * batch + [400], heads)
+    # heads in several groups (their keys do not fit L2 together): blocks with keys again
+    # behind the blocks without
+    go(dims_of(V2, heads, BF), [3] * batch + [60], [0] * batch + [9000], heads)
+
+
 def test_queries_that_see_no_key():
     """lq > lk: the first lq - lk queries see nothing and get zeros and -inf."""
     new, total = [200, 5, 130, 300], [72, 0, 1, 20]
