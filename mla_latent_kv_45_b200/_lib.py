@@ -1,5 +1,9 @@
 """ctypes binding of ``libmla_b200.so`` (declared in ``include/mla.h``).
 
+The prompt calls, whose small sizes take less time than ten tensors' checks in Python, go
+through the same checks in C++ (``csrc/marshal.cpp``) first; those decline what is not
+exactly right, and the checks here then say what is wrong.
+
 Argument marshalling only: every function here forwards torch tensors' device
 pointers and sizes to the C ABI call of the same name and raises ``MlaError``
 on a non-OK status.  There is no fallback: if the library is missing the
@@ -113,11 +117,12 @@ class PagedCache:
 
 
 _lib = None
+_marshal = None
 
 
 def lib() -> ctypes.CDLL:
     """Loads the library (raises if it has not been built)."""
-    global _lib
+    global _lib, _marshal
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is missing: run `python -m mla_latent_kv_45_b200.build`")
@@ -150,6 +155,10 @@ def lib() -> ctypes.CDLL:
             if name not in ("mla_workspace_size", "mla_prompt_workspace_size",
                             "mla_status_string"):
                 getattr(L, name).restype = i
+        from . import _marshal as m
+        m.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value
+                 for f in ("mla_prompt_append", "mla_cache_gather", "mla_prompt_attn")))
+        _marshal = m
         _lib = L
     return _lib
 
@@ -302,6 +311,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+def _address(stream):
+    """A given stream for the C++ checks: its address, of a stream that is on the current
+    device (they take tensors of that device only); None stays None."""
+    if stream is None:
+        return None
+    return stream.cuda_stream if stream.device_index == torch.cuda.current_device() else False
+
+
 def _on(fn: str, dev: int, ws: torch.Tensor, stream) -> int:
     """The stream to launch on (default: the device's current one), after a look at ws."""
     if ws is None or ws.get_device() != dev or not ws.is_contiguous():
@@ -337,7 +354,14 @@ def mla_prompt_append(dims: Dims, cache: PagedCache, x, gamma, cu_tokens, ctx_le
     ctx_lens ``[batch]`` int32 or None, q_rope and q_out ``[tokens, n_heads,
     d_rope]`` (any token and head strides; q_out may be q_rope) or None.
     """
-    fn, dt, i32 = "mla_prompt_append", dims.torch_dtype, torch.int32
+    fn = "mla_prompt_append"
+    lib()
+    if (s := _address(stream)) is not False:
+        st = _marshal.append(dims.c(), cache.pool, cache.block_table, x, gamma, cu_tokens,
+                             ctx_lens, q_rope, q_out, ws, s)
+        if st is not None:
+            return _ok(fn, st)
+    dt, i32 = dims.torch_dtype, torch.int32
     dev, n, batch = _device(fn, x), x.shape[0], cu_tokens.numel() - 1
     xd = x.dtype if x.dtype is torch.float32 else dt
     xp, xs = _rows(fn, xd, dev, x, "x", n, dims.d_c + dims.d_rope)
@@ -361,7 +385,14 @@ def mla_cache_gather(dims: Dims, cache: PagedCache, cu_rows, first_rows, rows,
                      ws: torch.Tensor = None, stream=None):
     """rows ``[n, d_c + d_rope]``: each sequence's cached rows from first_rows[b] (None: 0) on,
     packed at cu_rows ``[batch + 1]``; int8 rows come back as the values they hold."""
-    fn, i32 = "mla_cache_gather", torch.int32
+    fn = "mla_cache_gather"
+    lib()
+    if (s := _address(stream)) is not False:
+        st = _marshal.gather(dims.c(), cache.pool, cache.block_table, cu_rows, first_rows, rows,
+                             ws, s)
+        if st is not None:
+            return _ok(fn, st)
+    i32 = torch.int32
     dev, n, batch = _device(fn, rows), rows.shape[0], cu_rows.numel() - 1
     handle = _on(fn, dev, ws, stream)
     _call(fn, dev, lib().mla_cache_gather, ctypes.byref(dims.c()),
@@ -382,7 +413,13 @@ def mla_prompt_attn(dims: Dims, q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, o
     ``[batch + 1]`` int32, out ``[n_q, n_heads, d_v]``, lse ``[n_q, n_heads]``
     fp32 or None.
     """
-    fn, dt, i32, H = "mla_prompt_attn", dims.torch_dtype, torch.int32, dims.n_heads
+    fn = "mla_prompt_attn"
+    lib()
+    if (s := _address(stream)) is not False:
+        st = _marshal.attn(dims.c(), q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, out, lse, ws, s)
+        if st is not None:
+            return _ok(fn, st)
+    dt, i32, H = dims.torch_dtype, torch.int32, dims.n_heads
     dev, n_q, n_k, off = _device(fn, q_nope), q_nope.shape[0], k_nope.shape[0], cu_q.shape
     n_kv = k_nope.shape[1]
     krp, krs = _rows(fn, dt, dev, k_rope, "k_rope", n_k, dims.d_rope)
