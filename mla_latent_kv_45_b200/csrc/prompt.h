@@ -135,7 +135,7 @@ struct PromptAttnArgs {
   // Keys of few blocks cut into pieces: [kPromptParts][256 rows][128], and the rows'
   // m (log2 units) and l.
   float *part_O, *part_m, *part_l;
-  PromptJoin *join;   // [max_items]
+  PromptJoin *join;  // [max_items]
   void *out;   // [n_q][n_heads][d_v]
   float *lse;  // [n_q][n_heads] or nullptr
   int *err;
@@ -146,7 +146,7 @@ constexpr int kPromptTileSm100 = 256;   // rows of an item: (token, head) pairs
 // Up to this many items the sm_100a kernel plans for itself and needs no plan kernel.
 constexpr int kPromptOwnItems = 512;
 
-template <class T>
+// fp32
 cudaError_t launch_prompt_attn_simt(const PromptAttnArgs &a, cudaStream_t s);
 
 namespace sm100 {

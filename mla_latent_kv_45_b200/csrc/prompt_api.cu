@@ -52,7 +52,7 @@ constexpr size_t kPartBytes = sizeof(float) * 256 * (128 + 2);   // O, m and l o
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Bytes up to the partial results (20 MB, bf16), which small calls over long keys use.
+// bf16: bytes up to the partial results (20 MB), which small calls over long keys use.
 // They are always part of the size, so that a workspace for many tokens does for few.
 size_t plan_bytes(const mla_dims &d, int batch, int n_tokens) {
   return align256(kItemsAt +
@@ -61,7 +61,7 @@ size_t plan_bytes(const mla_dims &d, int batch, int n_tokens) {
 }
 
 size_t prompt_ws_bytes(const mla_dims &d, int batch, int n_tokens) {
-  return plan_bytes(d, batch, n_tokens) + (d.dtype == MLA_BF16 ? kPromptParts * kPartBytes : 0);
+  return d.dtype == MLA_BF16 ? plan_bytes(d, batch, n_tokens) + kPromptParts * kPartBytes : kItemsAt;
 }
 
 mla_status check_ws(const void *ws, size_t ws_bytes, size_t need) {
@@ -216,7 +216,7 @@ mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, in
   pa.err = err_of(ws);
   const long max_items = prompt_max_items(n_q, batch, pa.tile);
   pa.max_items = (int)max_items;
-  if (d.dtype == MLA_FP32 || max_items > kPromptOwnItems)
+  if (d.dtype == MLA_BF16 && max_items > kPromptOwnItems)
     MLA_TRY(cuda_ok(launch_prompt_plan(pa, s)));
   PromptAttnArgs a{};
   a.q_nope = view(q_nope, n_q, d.n_heads, d.d_nope);
@@ -251,7 +251,7 @@ mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, in
   a.out = out;
   a.lse = lse;
   a.err = pa.err;
-  if (d.dtype == MLA_FP32) return cuda_ok(launch_prompt_attn_simt<float>(a, s));
+  if (d.dtype == MLA_FP32) return cuda_ok(launch_prompt_attn_simt(a, s));
   return cuda_ok(sm100::launch_prompt_attn(a, s));
 }
 

@@ -494,9 +494,52 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(PromptPlanArgs a) {
 
 constexpr int kSimtKeys = 32;
 
+// Block `at` of the call's blocks in the order of the sequences (false: there are fewer),
+// found by the CTA's 128 threads, a thread a sequence: its blocks are counted and summed
+// up.  (A plan of all blocks by a launch of its own cost 5 us more than this.)
+__device__ __forceinline__ bool simt_block(const PromptAttnArgs &a, int at, PromptItem &it) {
+  __shared__ PromptItem found;
+  __shared__ int warp_tot[4];
+  const int tid = threadIdx.x, lane = tid & 31;
+  int before = 0;      // blocks of the sequences before
+  for (int b0 = 0; b0 < a.batch; b0 += 128) {
+    const int b = b0 + tid;
+    int q0, lq, k0, lk, n = 0;
+    if (b < a.batch) {
+      if (prompt_seq(a.cu_q, a.cu_k, a.n_q, a.n_k, b, q0, lq, k0, lk))
+        n = (lq + kPromptTileSimt - 1) / kPromptTileSimt;
+      else if (at == 0)
+        set_error(a.err, kErrRange);
+    }
+    int v = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += x;
+    }
+    if (lane == 31) warp_tot[tid >> 5] = v;
+    __syncthreads();
+    int first = before + v - n, all = before;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      first += i < (tid >> 5) ? warp_tot[i] : 0;
+      all += warp_tot[i];
+    }
+    if (at >= first && at < first + n)
+      found = prompt_item(q0, lq, k0, lk, (at - first) * kPromptTileSimt, kPromptTileSimt);
+    __syncthreads();
+    // block 0 looks at every sequence's offsets
+    if (at < all && (at > 0 || b0 + 128 >= a.batch)) {
+      it = found;
+      return true;
+    }
+    before = all;
+  }
+  return false;
+}
+
 // One block of 16 rows of one head per CTA (128 threads), 32 keys at a time
 // through shared memory, one pass with the running maximum and sum.
-template <class T>
 __global__ void __launch_bounds__(128) prompt_attn_simt(PromptAttnArgs a) {
   extern __shared__ float sm[];
   const int dq = a.d_nope + a.d_rope, ldk = dq + 1;
@@ -506,19 +549,20 @@ __global__ void __launch_bounds__(128) prompt_attn_simt(PromptAttnArgs a) {
   float *ps = vs + kSimtKeys * a.d_v;       // [16][33]
   __shared__ float m_s[kPromptTileSimt], l_s[kPromptTileSimt], f_s[kPromptTileSimt];
   grid_dep_wait();
-  if ((int)blockIdx.x >= a.hdr->items) return;
-  const PromptItem it = a.items[blockIdx.x];
+  grid_dep_launch();
+  PromptItem it;
+  if (!simt_block(a, blockIdx.x, it)) return;
   const int h = blockIdx.y, kv = h / (a.n_heads / a.n_kv_heads), tid = threadIdx.x;
-  const T *qn = static_cast<const T *>(a.q_nope.ptr) + h * a.q_nope.head;
-  const T *qr = static_cast<const T *>(a.q_rope.ptr) + h * a.q_rope.head;
-  const T *kn = static_cast<const T *>(a.k_nope.ptr) + kv * a.k_nope.head;
-  const T *kr = static_cast<const T *>(a.k_rope);
-  const T *vp = static_cast<const T *>(a.v.ptr) + kv * a.v.head;
+  const float *qn = static_cast<const float *>(a.q_nope.ptr) + h * a.q_nope.head;
+  const float *qr = static_cast<const float *>(a.q_rope.ptr) + h * a.q_rope.head;
+  const float *kn = static_cast<const float *>(a.k_nope.ptr) + kv * a.k_nope.head;
+  const float *kr = static_cast<const float *>(a.k_rope);
+  const float *vp = static_cast<const float *>(a.v.ptr) + kv * a.v.head;
   for (int i = tid; i < it.rows * dq; i += blockDim.x) {
     const int r = i / dq, c = i % dq;
     const long t = it.q0 + r;
-    qs[i] = c < a.d_nope ? ld_f(qn + t * a.q_nope.token + c)
-                         : ld_f(qr + t * a.q_rope.token + c - a.d_nope);
+    qs[i] = c < a.d_nope ? qn[t * a.q_nope.token + c]
+                         : qr[t * a.q_rope.token + c - a.d_nope];
   }
   if (tid < kPromptTileSimt) {
     m_s[tid] = -INFINITY;
@@ -536,12 +580,12 @@ __global__ void __launch_bounds__(128) prompt_attn_simt(PromptAttnArgs a) {
     for (int i = tid; i < nk * dq; i += blockDim.x) {
       const int j = i / dq, c = i % dq;
       const long t = it.k0 + j0 + j;
-      ks[j * ldk + c] = c < a.d_nope ? ld_f(kn + t * a.k_nope.token + c)
-                                     : ld_f(kr + t * a.k_rope_stride + c - a.d_nope);
+      ks[j * ldk + c] = c < a.d_nope ? kn[t * a.k_nope.token + c]
+                                     : kr[t * a.k_rope_stride + c - a.d_nope];
     }
     for (int i = tid; i < nk * a.d_v; i += blockDim.x) {
       const int j = i / a.d_v, c = i % a.d_v;
-      vs[i] = ld_f(vp + (it.k0 + j0 + j) * a.v.token + c);
+      vs[i] = vp[(it.k0 + j0 + j) * a.v.token + c];
     }
     __syncthreads();
     // scores: warp w has rows w, w + 4, ...; lane = key
@@ -586,7 +630,7 @@ __global__ void __launch_bounds__(128) prompt_attn_simt(PromptAttnArgs a) {
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
     const int c = c_o + 8 * j;
-    if (j < cols && c < a.d_v) static_cast<T *>(a.out)[at * a.d_v + c] = st_cast<T>(acc[j] * inv);
+    if (j < cols && c < a.d_v) static_cast<float *>(a.out)[at * a.d_v + c] = acc[j] * inv;
   }
   if (a.lse && c_o == 0) a.lse[at] = l == 0.f ? -INFINITY : m_s[r_o] + logf(l);
 }
@@ -630,20 +674,18 @@ cudaError_t launch_prompt_plan(const PromptPlanArgs &a, cudaStream_t s) {
   return launch_pdl(prompt_plan_kernel, dim3(1), dim3(kBins), 0, s, a);
 }
 
-template <class T>
 cudaError_t launch_prompt_attn_simt(const PromptAttnArgs &a, cudaStream_t s) {
   const int dq = a.d_nope + a.d_rope;
   const size_t smem = sizeof(float) * (kPromptTileSimt * dq + kSimtKeys * (dq + 1) +
                                        kSimtKeys * a.d_v + kPromptTileSimt * 33);
   static api::PerDeviceOnce once;
   const cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(prompt_attn_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(prompt_attn_simt, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 120 * 1024);
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(prompt_attn_simt<T>, dim3((unsigned)a.max_items, a.n_heads), dim3(128), smem, s,
+  return launch_pdl(prompt_attn_simt, dim3((unsigned)a.max_items, a.n_heads), dim3(128), smem, s,
                     a);
 }
-template cudaError_t launch_prompt_attn_simt<float>(const PromptAttnArgs &, cudaStream_t);
 
 }  // namespace mla

@@ -411,3 +411,38 @@ def test_captured_and_replayed_with_other_lengths():
         torch.cuda.synchronize()
         assert L.mla_get_device_error(ws) == 0
         check_attn(dims, t, q, k, out, lse, str(q))
+
+
+@pytest.mark.parametrize("batch", [127, 128, 129, 300])
+def test_fp32_many_sequences(batch):
+    """A block finds its sequence 128 at a time."""
+    new = [(7 * i + 3 * batch) % 20 for i in range(batch)]
+    total = [n + (11 * i) % 30 for i, n in enumerate(new)]
+    go(dims_of(TINY, 2, F32), new, total, 1)
+    go(dims_of(TINY, 2, F32), [0] * (batch - 1) + [40], [3] * (batch - 1) + [40], 1)
+
+
+@pytest.mark.parametrize("at", [0, 5, 128, 299])
+def test_fp32_bad_offsets_skip_their_sequence(at):
+    batch, n = 300, 3
+    dims = dims_of(TINY, 2, F32)
+    cu = offsets([n] * batch)
+    t = attn_inputs(dims, cu[-1], cu[-1], 2, 23)
+    ws = workspace(dims, batch, cu[-1])
+    want, want_lse = run_attn(dims, t, cu, cu, ws=ws)
+    bad_q = list(cu)
+    bad_q[at + 1 if at == batch - 1 else at] += 10000 if at == batch - 1 else -10000
+    out, lse = torch.full_like(want, 7.0), torch.full_like(want_lse, 7.0)
+    L.mla_prompt_attn(dims, t["q_nope"], t["q_rope"], t["k_nope"], t["k_rope"], t["v"],
+                      i32(bad_q), i32(cu), out, lse, ws)
+    assert L.mla_get_device_error(ws) == 6
+    # the sequences on both sides of the bad offset are skipped
+    skipped = {at} if at in (0, batch - 1) else {at - 1, at}
+    for b in range(batch):
+        rows = slice(n * b, n * b + n)
+        if b in skipped:
+            assert (out[rows] == 7).all() and (lse[rows] == 7).all(), b
+        else:
+            assert torch.equal(out[rows], want[rows]) and torch.equal(lse[rows], want_lse[rows]), b
+    again, _ = run_attn(dims, t, cu, cu, ws=ws)
+    assert torch.equal(again, want)
