@@ -180,13 +180,14 @@ __device__ __forceinline__ int tile_steps(const PromptItem &it, int t, int lg) {
 // pieces as there are CTAs for, by their number of steps (at least kMinSteps a
 // piece).  A piece is an item of its own whose keys are a range of the block's; it
 // leaves an unnormalised result that the join kernel merges.
-// `scratch`: 4.2 KB of shared memory.
+// `scratch`: 12.4 KB of shared memory.
 __device__ __forceinline__ int own_plan(const PromptAttnArgs &a, PromptItem *list, int *scratch,
                                         bool split) {
   static_assert(kThreads == kPromptOwnItems, "a thread an item");
   int *first = scratch;          // [512] items before the sequence
   int *keys = first + 512;       // [512] of item i, before sorting
   int *warp_tot = keys + 512;    // [16]
+  int4 *seq = reinterpret_cast<int4 *>(warp_tot + 16);   // [512] q0, lq, k0, lk
   const int tid = threadIdx.x, lane = tid & 31, tile = kPromptTileSm100 >> a.pack_log2;
   int q0, lq, k0, lk, n = 0;
   if (tid < a.batch) {
@@ -194,6 +195,7 @@ __device__ __forceinline__ int own_plan(const PromptAttnArgs &a, PromptItem *lis
       n = (lq + tile - 1) / tile;
     else if (blockIdx.x == 0)
       set_error(a.err, kErrRange);
+    seq[tid] = make_int4(q0, lq, k0, lk);
   }
   int v = n;
 #pragma unroll
@@ -219,8 +221,8 @@ __device__ __forceinline__ int own_plan(const PromptAttnArgs &a, PromptItem *lis
 #pragma unroll
     for (int step = kPromptOwnItems / 2; step > 0; step >>= 1)
       if (b + step < a.batch && first[b + step] <= tid) b += step;
-    prompt_seq(a.cu_q, a.cu_k, a.n_q, a.n_k, b, q0, lq, k0, lk);
-    it = prompt_item(q0, lq, k0, lk, (tid - first[b]) * tile, tile);
+    const int4 x = seq[b];
+    it = prompt_item(x.x, x.y, x.z, x.w, (tid - first[b]) * tile, tile);
     mine = prompt_keys(it);
   }
   keys[tid] = mine;
