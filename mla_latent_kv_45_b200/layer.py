@@ -115,6 +115,8 @@ class PromptLayer:
 
     def __init__(self, dims: L.Dims, weights: dict, batch: int, tokens: int, rows: int,
                  device="cuda"):
+        if min(batch, tokens, rows) < 1:
+            raise ValueError(f"no buffers for {batch} sequences, {tokens} tokens, {rows} rows")
         nbytes = L.mla_prompt_workspace_size(dims, batch, tokens)
         if nbytes == 0:
             raise ValueError("unsupported dims for the workspace")
@@ -153,6 +155,8 @@ class PromptLayer:
         ctx_lens[b] + cu_tokens[b+1] - cu_tokens[b] (int32 device tensors, all read
         on the device).  cache.seq_lens is not read.
         """
+        if h.shape[0] != self.tokens:     # (the products would resize their outputs)
+            raise ValueError(f"h has {h.shape[0]} tokens, the buffers are for {self.tokens}")
         s = stream if stream is not None else torch.cuda.current_stream(self.ws.device)
         d = self.dims
         with torch.cuda.stream(s):

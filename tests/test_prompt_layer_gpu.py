@@ -168,3 +168,21 @@ def test_captured_chunk_replays_with_other_lengths_and_on_another_stream():
     got = layer.step(cache, h, cu, ctx, rows, side)
     side.synchronize()
     assert torch.equal(got[:14], want[:14])
+
+
+def test_refuses_sizes_that_its_buffers_do_not_have():
+    wl = synth.TINY
+    dims, Wd = lib_dims(wl), dev_weights(synth.make_weights(wl), wl)
+    for sizes in ((0, 4, 4), (1, 0, 4), (1, 4, 0)):
+        with pytest.raises(ValueError):
+            PromptLayer(dims, Wd, *sizes)
+    layer = PromptLayer(dims, Wd, 1, 4, 4)
+    cache = L.PagedCache(torch.zeros(1, 16, wl.row, device="cuda"), i32([[0]]), None)
+    x = layer.x.data_ptr()
+    for n in (3, 5):
+        with pytest.raises(ValueError):
+            layer.step(cache, torch.zeros(n, wl.d_model, device="cuda"), i32([0, n]), None,
+                       i32([0, n]))
+    assert layer.x.shape[0] == 4 and layer.x.data_ptr() == x
+    layer.step(cache, torch.ones(4, wl.d_model, device="cuda"), i32([0, 4]), None, i32([0, 4]))
+    assert layer.device_error() == 0
