@@ -80,6 +80,7 @@ constexpr int kPromptParts = 148;
 struct PromptPlanArgs {
   const int32_t *cu_q, *cu_k;
   int batch, n_q, n_k, tile;
+  int few_tokens;     // sequences of so many tokens at most have no items (0: all have)
   int max_items;      // prompt_max_items(n_q, batch, tile); offsets that overlap could ask for more
   PromptPlanHeader *hdr;
   PromptItem *items;  // [max_items]
@@ -132,6 +133,7 @@ struct PromptAttnArgs {
   const PromptItem *items;
   const int32_t *cu_q, *cu_k;
   int batch;
+  int few_tokens;  // sequences of so many tokens at most are left to prompt_few_kernel (0: none)
   // Keys of few blocks cut into pieces: [kPromptParts][256 rows][128], and the rows'
   // m (log2 units) and l.
   float *part_O, *part_m, *part_l;
@@ -143,11 +145,16 @@ struct PromptAttnArgs {
 
 constexpr int kPromptTileSimt = 16;
 constexpr int kPromptTileSm100 = 256;   // rows of an item: (token, head) pairs
+constexpr int kPromptFewRows = 16;      // rows of a sequence and key head that prompt_few_kernel takes
+constexpr int kPromptSplitKeys = 1024;  // fewest keys of a call whose blocks are cut into pieces
 // Up to this many items the sm_100a kernel plans for itself and needs no plan kernel.
 constexpr int kPromptOwnItems = 512;
 
 // fp32
 cudaError_t launch_prompt_attn_simt(const PromptAttnArgs &a, cudaStream_t s);
+
+// bf16, d_nope = d_v = 128, d_rope = 64: the sequences of at most few_tokens tokens
+cudaError_t launch_prompt_few(const PromptAttnArgs &a, cudaStream_t s);
 
 namespace sm100 {
 // bf16, d_nope = d_v = 128, d_rope = 64, items of at most kPromptTileSm100 rows

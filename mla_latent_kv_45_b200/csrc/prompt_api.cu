@@ -42,6 +42,19 @@ int least_tile_tokens(const mla_dims &d) {
   return least;
 }
 
+// Tokens up to which a sequence goes to the kernel for few rows (bf16; 0: that kernel is not
+// launched).  The lengths are on the device only, so the average decides whether it
+// is worth a launch.  Few blocks whose keys may be long are cut into pieces instead.
+int few_tokens(const mla_dims &d, int rep, int batch, int n_q, int n_k, long max_items) {
+  if (d.dtype != MLA_BF16 || rep > kPromptFewRows) return 0;
+  const int most = kPromptFewRows / rep;
+  const long work = max_items * (d.n_heads >> pack_log2(rep));
+  if ((long)batch * (d.n_heads / rep) > 0x7fffffffL) return 0;     // a grid's blocks
+  if (n_q > (long)most * batch || (2 * work <= kPromptParts && n_k >= 2 * kPromptSplitKeys))
+    return 0;
+  return most;
+}
+
 // The error word and the plan header share the first 256 bytes (the part that
 // mla_workspace_init clears); the plan's items follow.  The header holds counters that
 // outlive a call, so it lies where no other call of the library writes: a workspace
@@ -216,7 +229,10 @@ mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, in
   pa.err = err_of(ws);
   const long max_items = prompt_max_items(n_q, batch, pa.tile);
   pa.max_items = (int)max_items;
-  if (d.dtype == MLA_BF16 && max_items > kPromptOwnItems)
+  pa.few_tokens = few_tokens(d, rep, batch, n_q, n_k, max_items);
+  // (where no sequence can have more tokens, there is nothing to plan)
+  const bool only_few = n_q <= pa.few_tokens;
+  if (d.dtype == MLA_BF16 && max_items > kPromptOwnItems && !only_few)
     MLA_TRY(cuda_ok(launch_prompt_plan(pa, s)));
   PromptAttnArgs a{};
   a.q_nope = view(q_nope, n_q, d.n_heads, d.d_nope);
@@ -239,6 +255,7 @@ mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, in
   a.cu_q = cu_q;
   a.cu_k = cu_k;
   a.batch = batch;
+  a.few_tokens = pa.few_tokens;
   a.scale = api::softmax_scale(d);
   a.hdr = pa.hdr;
   a.items = pa.items;
@@ -252,7 +269,8 @@ mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, in
   a.lse = lse;
   a.err = pa.err;
   if (d.dtype == MLA_FP32) return cuda_ok(launch_prompt_attn_simt(a, s));
-  return cuda_ok(sm100::launch_prompt_attn(a, s));
+  if (a.few_tokens > 0) MLA_TRY(cuda_ok(launch_prompt_few(a, s)));
+  return only_few ? MLA_OK : cuda_ok(sm100::launch_prompt_attn(a, s));
 }
 
 }  // extern "C"

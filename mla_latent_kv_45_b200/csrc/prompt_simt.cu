@@ -441,6 +441,7 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(PromptPlanArgs a) {
         if (lane == 0) set_error(a.err, kErrRange);
         continue;
       }
+      if (lq <= a.few_tokens) continue;
       for (int r = lane * a.tile; r < lq; r += 32 * a.tile) {
         const PromptItem it = prompt_item(q0, lq, k0, lk, r, a.tile);
         f(it, prompt_keys(it));
@@ -450,7 +451,8 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(PromptPlanArgs a) {
   int top = 1;
   for (int b = tid; b < a.batch; b += blockDim.x) {
     int q0, lq, k0, lk;
-    if (prompt_seq(a.cu_q, a.cu_k, a.n_q, a.n_k, b, q0, lq, k0, lk) && lq > 0) top = max(top, lk);
+    if (prompt_seq(a.cu_q, a.cu_k, a.n_q, a.n_k, b, q0, lq, k0, lk) && lq > a.few_tokens)
+      top = max(top, lk);
   }
   atomicMax(&top_s, top);
   __syncthreads();

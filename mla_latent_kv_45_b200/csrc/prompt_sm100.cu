@@ -29,6 +29,7 @@
 //    thread for both was the bottleneck: every wait of one tile held up the other).
 //  * Work comes from a counter: the CTAs are persistent and fetch (block, head)
 //    pairs, blocks with most keys first.
+//  * Sequences of few rows may be left to prompt_few.cu: they have no items.
 //  * Every wait is bounded as in the decode kernel; on expiry the error word is set.
 //
 // What bounds it: a step takes about 2180 cycles.  The MMAs read 196 KB of operands
@@ -53,7 +54,6 @@ using bf16 = __nv_bfloat16;
 constexpr int kRows = 128;              // query rows of a tile
 constexpr int kKeys = 80;               // keys of a step
 constexpr int kMinSteps = 4;            // of a piece of a block's keys
-constexpr int kSplitKeys = 1024;        // fewest keys of a call whose blocks are cut
 constexpr int kSched = 3;               // work items in flight between the warps
 constexpr int kWarpOut = 8;             // warps 8-11
 constexpr int kWarpLoad = 12, kWarpFix = 13, kWarpMma = 14, kWarps = 16;   // MMA: 14, 15
@@ -192,7 +192,7 @@ __device__ __forceinline__ int own_plan(const PromptAttnArgs &a, PromptItem *lis
   int q0, lq, k0, lk, n = 0;
   if (tid < a.batch) {
     if (prompt_seq(a.cu_q, a.cu_k, a.n_q, a.n_k, tid, q0, lq, k0, lk))
-      n = (lq + tile - 1) / tile;
+      n = lq > a.few_tokens ? (lq + tile - 1) / tile : 0;
     else if (blockIdx.x == 0)
       set_error(a.err, kErrRange);
     seq[tid] = make_int4(q0, lq, k0, lk);
@@ -931,7 +931,7 @@ cudaError_t launch_prompt_attn(const PromptAttnArgs &a, cudaStream_t s) {
   const long work = a.max_items * packs;
   // Few blocks with long keys: see own_plan.  (The bounds that the host knows decide;
   // what the lengths then allow is decided on the device.)
-  const bool split = 2 * work <= sms && 2 * work <= kPromptParts && a.n_k >= kSplitKeys;
+  const bool split = 2 * work <= sms && 2 * work <= kPromptParts && a.n_k >= kPromptSplitKeys;
   const float scale_log2 = a.scale * 1.4426950408889634f;
   const long ctas = split ? (sms < kPromptParts ? sms : kPromptParts) : work < sms ? work : sms;
   e = launch_pdl(prompt_attn_kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, s, qn, qr, kn,
