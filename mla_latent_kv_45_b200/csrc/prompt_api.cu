@@ -44,7 +44,7 @@ int least_tile_tokens(const mla_dims &d) {
 
 // Tokens up to which a sequence goes to the kernel for few rows (bf16; 0: that kernel is not
 // launched).  The lengths are on the device only, so the average decides whether it
-// is worth a launch (100 sequences of 0-8 tokens, 128 heads: 82 us, 223 without it).  Few
+// is worth a launch (100 sequences of 0-8 tokens, 128 heads: 79 us, 223 without it).  Few
 // blocks whose keys may be long are cut into pieces instead: one token over 1000, 1500
 // and 1990 rows takes 12.8, 16.8 and 20.8 us here and 18.5, 16.3 and 18.0 there with 16 heads,
 // 13.0, 17.1 and 21.2 here and 18.9, 21.1 and 24.0 there with 64.

@@ -285,6 +285,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lg = a.pack_log2, tt = kRows >> lg;   // heads a token has in a tile, tokens of a tile
 
+  const bool own = a.max_items <= kPromptOwnItems;    // (a.batch is not above a.max_items)
+  if (a.few_tokens > 0) {
+    // The other kernel may have taken every sequence: nothing is set up then.
+    grid_dep_wait();
+    const int b = threadIdx.x;
+    const bool some = own ? b < a.batch && a.cu_q[b + 1] - a.cu_q[b] > a.few_tokens
+                          : a.hdr->items > 0;
+    if (!__syncthreads_or(some)) {
+      grid_dep_launch();
+      if (split && blockIdx.x == 0 && b < a.max_items) a.join[b] = PromptJoin{0, 0, 0, 0};
+      return;
+    }
+  }
+
   // The swizzled boxes need a 1024-byte boundary, which the dynamic shared memory
   // starts on (there is no static part in front of it).
   if (smem_u32(smem) & 1023) {
@@ -334,7 +348,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = bars->tmem_base;
   grid_dep_wait();     // nothing of the call is read before this
   grid_dep_launch();
-  const bool own = a.max_items <= kPromptOwnItems;
   PromptItem *const own_items = reinterpret_cast<PromptItem *>(smem + kOffItems);
   const int items = own ? own_plan(a, own_items, reinterpret_cast<int *>(smem + kOffOut), split)
                         : a.hdr->items;
