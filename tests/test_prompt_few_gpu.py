@@ -175,3 +175,22 @@ def test_captured_and_replayed_with_other_lengths():
             assert torch.equal(out, first)
         check_attn(dims, t, q, k, out, lse)
         assert (out[q[-1]:] == 7).all()
+
+
+@pytest.mark.parametrize("long", [0, 17, 200])
+def test_beside_blocks_whose_keys_are_cut(long):
+    """Few blocks over more than 1024 keys: those that the other kernel leaves are cut and
+    joined, and where it leaves none the join finds nothing to do."""
+    new, total = [1, 2, 16] * 7 + [long], [60] * 21 + [long + 300 if long else 0]
+    dims, t, cu_q, cu_k, out, lse = go(new, total, 2, 2, seed=long)
+    ws = workspace(dims, 22, cu_q[-1])
+    for _ in range(3):
+        again, lse2 = run_attn(dims, t, cu_q, cu_k, ws=ws)
+        assert torch.equal(again, out) and torch.equal(lse2, lse)
+    # the same workspace for a call that is cut, then for one that is not
+    go([64], [1500], 2, 2)
+    big = attn_inputs(dims, 64, 1500, 2, 5)
+    o, e = run_attn(dims, big, [0, 64], [0, 1500], ws=ws)
+    check_attn(dims, big, [0, 64], [0, 1500], o, e)
+    again, lse2 = run_attn(dims, t, cu_q, cu_k, ws=ws)
+    assert torch.equal(again, out) and torch.equal(lse2, lse)
