@@ -428,11 +428,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m_new = top <= m + 8.0f && m != -INFINITY ? m : top;
         const bool moved = m_new != m;
         const float base = m_new == -INFINITY ? 0.f : m_new;   // a row that sees nothing so far
-        // P is free and O complete once the previous step's product is
+        // P is free and O complete once the previous step's product is; the product read P
+        // from TMEM asynchronously, so the stores below need the fence whether m moved or not
         if (ns > 0) ok = wait_all(&bars->pv_done[t], (ns - 1) & 1);
         if (!ok) break;
+        tc_fence_after();
         if (j > 0 && __any_sync(0xffffffffu, moved)) {
-          tc_fence_after();
           const float f = moved ? ex2(m - base) : 1.f;
           l *= f;
 #pragma unroll 1
