@@ -360,6 +360,16 @@ mla_status mla_get_device_error(void *ws, mla_stream_t stream);
  * concurrent mla_absorb_q calls.  No page describes this; it exists for tests. */
 mla_status mla_debug_absorb_timeout(int enable, unsigned wait_limit_us);
 
+/* Test hook, not for production use: with enable != 0, every later mla_prompt_attn
+ * (MLA_BF16) call bounds each wait between its kernel's warps by wait_limit_us
+ * microseconds (instead of 2 s and 100 ns a key), so that a block over many keys, whose
+ * output warps wait for all of its steps, runs into the limit.  The kernel then records
+ * MLA_ERR_TIMEOUT in the workspace error word, waits for the loads and MMAs it
+ * issued and exits (out and lse are not valid); the workspace stays usable.  A call that
+ * is captured into a graph keeps the limit it was captured with.  enable = 0 restores
+ * normal operation.  Process-wide.  No page describes this; it exists for tests. */
+mla_status mla_debug_prompt_timeout(int enable, unsigned wait_limit_us);
+
 /* Static, NUL-terminated description of a status code. */
 const char *mla_status_string(mla_status status);
 

@@ -36,7 +36,7 @@ EXPORTS = ("mla_workspace_size", "mla_workspace_init", "mla_cache_append", "mla_
            "mla_decode_attn_noalloc", "mla_unabsorb_out", "mla_prompt_workspace_size",
            "mla_prompt_append", "mla_cache_gather", "mla_prompt_attn",
            "mla_noalloc_get_device_error", "mla_get_device_error", "mla_debug_absorb_timeout",
-           "mla_status_string")
+           "mla_debug_prompt_timeout", "mla_status_string")
 
 
 class MlaError(RuntimeError):
@@ -149,6 +149,7 @@ def lib() -> ctypes.CDLL:
         L.mla_get_device_error.argtypes = [vp, vp]
         L.mla_noalloc_get_device_error.argtypes = [vp]
         L.mla_debug_absorb_timeout.argtypes = [i, ctypes.c_uint]
+        L.mla_debug_prompt_timeout.argtypes = [i, ctypes.c_uint]
         L.mla_status_string.argtypes = [i]
         L.mla_status_string.restype = ctypes.c_char_p
         for name in EXPORTS:
@@ -445,6 +446,11 @@ def mla_noalloc_get_device_error(stream=None) -> int:
 def mla_debug_absorb_timeout(enable: bool, wait_limit_us: int = 0):
     """Test hook: make the absorption kernel's q_C hand-off wait run out (see mla.h)."""
     _ok("mla_debug_absorb_timeout", lib().mla_debug_absorb_timeout(int(enable), wait_limit_us))
+
+
+def mla_debug_prompt_timeout(enable: bool, wait_limit_us: int = 0):
+    """Test hook: limit the prompt attention kernel's waits (see mla.h)."""
+    _ok("mla_debug_prompt_timeout", lib().mla_debug_prompt_timeout(int(enable), wait_limit_us))
 
 
 def mla_get_device_error(ws: torch.Tensor, stream=None) -> int:

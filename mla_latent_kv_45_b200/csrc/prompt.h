@@ -141,6 +141,7 @@ struct PromptAttnArgs {
   void *out;   // [n_q][n_heads][d_v]
   float *lse;  // [n_q][n_heads] or nullptr
   int *err;
+  uint64_t wait_ns;  // sm_100a: limit of a wait between the kernel's warps
 };
 
 constexpr int kPromptTileSimt = 16;

@@ -1,5 +1,7 @@
 // Host side of the prompt calls declared in include/mla.h: argument checks,
 // workspace layout and dispatch.  Nothing here allocates or synchronises.
+#include <atomic>
+
 #include <cuda_runtime.h>
 
 #include "api_checks.h"
@@ -84,6 +86,16 @@ mla_status check_ws(const void *ws, size_t ws_bytes, size_t need) {
   if (!ws) return MLA_ERR_INVALID_ARG;
   if (!aligned16(ws)) return MLA_ERR_ALIGNMENT;
   return ws_bytes < need ? MLA_ERR_WORKSPACE : MLA_OK;
+}
+
+// Limit of a wait between the attention kernel's warps.  The longest one is for an item
+// by the warps that write its output: a step of 80 keys takes 1.2 us, so 100 ns a key beside
+// the 2 s leave a factor of six.  (0: no test hook, see mla_debug_prompt_timeout.)
+std::atomic<unsigned long long> g_debug_wait_ns{0};
+
+uint64_t wait_limit_ns(int n_k) {
+  const unsigned long long d = g_debug_wait_ns.load(std::memory_order_relaxed);
+  return d ? d : 2000000000ull + 100ull * (unsigned)n_k;
 }
 
 int *err_of(void *ws) { return static_cast<int *>(ws); }
@@ -271,9 +283,16 @@ mla_status mla_prompt_attn(const mla_dims *dims, int batch, int n_q, int n_k, in
   a.out = out;
   a.lse = lse;
   a.err = pa.err;
+  a.wait_ns = wait_limit_ns(n_k);
   if (d.dtype == MLA_FP32) return cuda_ok(launch_prompt_attn_simt(a, s));
   if (a.few_tokens > 0) MLA_TRY(cuda_ok(launch_prompt_few(a, s)));
   return only_few ? MLA_OK : cuda_ok(sm100::launch_prompt_attn(a, s));
+}
+
+mla_status mla_debug_prompt_timeout(int enable, unsigned wait_limit_us) {
+  if (enable && wait_limit_us == 0) return MLA_ERR_INVALID_ARG;
+  g_debug_wait_ns.store(enable ? 1000ull * wait_limit_us : 0);
+  return MLA_OK;
 }
 
 }  // extern "C"

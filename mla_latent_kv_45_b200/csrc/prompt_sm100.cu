@@ -30,7 +30,8 @@
 //  * Work comes from a counter: the CTAs are persistent and fetch (block, head)
 //    pairs, blocks with most keys first.
 //  * Sequences of few rows may be left to prompt_few.cu: they have no items.
-//  * Every wait is bounded as in the decode kernel; on expiry the error word is set.
+//  * Every wait is bounded (PromptAttnArgs::wait_ns); on expiry the error word is set, the
+//    warps stop, and the loading warp and the MMA threads wait for what they have in flight.
 //
 // What bounds it: a step takes about 2180 cycles.  The MMAs read 196 KB of operands
 // from shared memory in it and TMA writes 50 KB there, which at 128 bytes a cycle is
@@ -58,7 +59,7 @@ constexpr int kSched = 3;               // work items in flight between the warp
 constexpr int kWarpOut = 8;             // warps 8-11
 constexpr int kWarpLoad = 12, kWarpFix = 13, kWarpMma = 14, kWarps = 16;   // MMA: 14, 15
 constexpr int kThreads = 32 * kWarps;
-constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr uint64_t kDrainNs = 2000000000ull;   // for copies and products in flight at the end
 constexpr uint32_t kSleepNs = 20000;
 
 // Shared memory: boxes of 64 columns (128 bytes, 128-byte swizzle)
@@ -110,6 +111,7 @@ static_assert(sizeof(Bars) <= 1024, "barrier region");
 struct Ctx {
   Bars *bars;
   int *err;
+  uint64_t limit;   // of a wait, ns
 };
 
 __device__ __forceinline__ bool wait_bar(const Ctx &c, uint64_t *bar, uint32_t parity) {
@@ -119,7 +121,7 @@ __device__ __forceinline__ bool wait_bar(const Ctx &c, uint64_t *bar, uint32_t p
   while (true) {
     if (mbar_try_wait(a, parity)) return true;
     if (c.bars->abort) return false;
-    if (globaltimer() - t0 > kTimeoutNs) {
+    if (globaltimer() - t0 > c.limit) {
       set_error(c.err, kErrTimeout);
       c.bars->abort = 1;
       return false;
@@ -132,7 +134,7 @@ __device__ __forceinline__ void drain_bar(uint64_t *bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
   const uint64_t t0 = globaltimer();
   while (!mbar_try_wait_sleep(a, parity, kSleepNs))
-    if (globaltimer() - t0 > kTimeoutNs) return;
+    if (globaltimer() - t0 > kDrainNs) return;
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const bool split) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars *bars = reinterpret_cast<Bars *>(smem + kOffBar);
-  const Ctx ctx{bars, a.err};
+  const Ctx ctx{bars, a.err, a.wait_ns};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lg = a.pack_log2, tt = kRows >> lg;   // heads a token has in a tile, tokens of a tile
 
@@ -665,17 +667,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && !bars->abort && gv < gk) load_v();
       // no CTA asks for work any more once all have been here
       if (atomicInc(&a.hdr->done, gridDim.x - 1) == gridDim.x - 1) a.hdr->next = 0;
-      if (bars->abort) {
-        // what is in flight must land before the CTA ends
-        for (int g = max(0, gk - 2); g < gk; ++g) drain_bar(&bars->k_full[g & 1], (g >> 1) & 1);
-        for (int g = max(0, gv - 2); g < gv; ++g)
-          if (tail[g & 1])
-            drain_bar(&bars->v_raw[g & 1], (raw[g & 1] - 1) & 1);
-          else
-            drain_bar(&bars->v_full[g & 1], (g >> 1) & 1);
-        for (int t = 0; t < 2; ++t)
-          if (nq[t] > 0) drain_bar(&bars->q_full[t], (nq[t] - 1) & 1);
-      }
+      // What is in flight must land before the CTA ends, and another warp's wait may run out
+      // after this one is through, so these are waited for whether one has or not.
+      for (int g = max(0, gk - 2); g < gk; ++g) drain_bar(&bars->k_full[g & 1], (g >> 1) & 1);
+      for (int g = max(0, gv - 2); g < gv; ++g)
+        if (tail[g & 1])
+          drain_bar(&bars->v_raw[g & 1], (raw[g & 1] - 1) & 1);
+        else
+          drain_bar(&bars->v_full[g & 1], (g >> 1) & 1);
+      for (int t = 0; t < 2; ++t)
+        if (nq[t] > 0) drain_bar(&bars->q_full[t], (nq[t] - 1) & 1);
     }
   } else if (warp == kWarpFix) {
     // Rows behind a sequence's last key belong to another sequence and may hold
