@@ -294,7 +294,8 @@ mla_status mla_cache_gather(const mla_dims *dims, const mla_paged_cache *cache, 
  * where head h reads the keys and values of head h / (n_heads / n_kv_heads): one
  * key head per query head as MLA expands them, or grouped heads.  k_rope is
  * shared by all heads.  A query that sees no key (lq > lk) gets out = 0,
- * lse = -inf, and that is no error.
+ * lse = -inf, and that is no error; one whose scores are all -inf gets what the
+ * formula gives, out = 0 / 0 = NaN and lse = -inf.
  * q_nope: [n_q][n_heads][d_nope]; q_rope: [n_q][n_heads][d_rope], rotated;
  * k_nope: [n_k][n_kv_heads][d_nope]; v: [n_k][n_kv_heads][d_v]; k_rope:
  * [n_k][d_rope], rotated, rows k_rope_stride elements apart; out:

@@ -63,8 +63,8 @@ struct PromptItem {
 // (of every pack of heads) make up its rows.
 struct PromptJoin {
   int q0, tokens, first, pieces;   // pieces == 0: nothing to join
+  int see;   // keys that the block's first token sees (may be <= 0); row r sees see + r
 };
-
 
 // The attention kernel's work counter, and the CTAs that are through with it: the
 // last one sets both back to zero, which mla_workspace_init has them start at.
@@ -144,6 +144,9 @@ struct PromptAttnArgs {
   uint64_t wait_ns;  // sm_100a: limit of a wait between the kernel's warps
 };
 
+// A row that sees keys, all of them with a score of -inf, gets 0 / 0 = NaN and lse = -inf as
+// the formula has it, unlike a row that sees none: each kernel asks what a row sees, not
+// whether its sum is zero.
 constexpr int kPromptTileSimt = 16;
 constexpr int kPromptTileSm100 = 256;   // rows of an item: (token, head) pairs
 constexpr int kPromptFewRows = 16;      // rows of a sequence and key head that prompt_few_kernel takes

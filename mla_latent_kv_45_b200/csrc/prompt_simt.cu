@@ -679,14 +679,15 @@ __global__ void __launch_bounds__(128) prompt_attn_simt(PromptAttnArgs a) {
   }
   __syncthreads();
   if (r_o >= it.rows) return;
-  const float l = l_s[r_o], inv = l == 0.f ? 0.f : 1.f / l;
+  const bool some = min(it.lk, it.see + r_o) > 0;      // the row sees a key
+  const float l = l_s[r_o], inv = some ? 1.f / l : 0.f;
   const long at = (long)(it.q0 + r_o) * a.n_heads + h;
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
     const int c = c_o + 8 * j;
     if (j < cols && c < a.d_v) static_cast<float *>(a.out)[at * a.d_v + c] = acc[j] * inv;
   }
-  if (a.lse && c_o == 0) a.lse[at] = l == 0.f ? -INFINITY : m_s[r_o] + logf(l);
+  if (a.lse && c_o == 0) a.lse[at] = some ? m_s[r_o] + logf(l) : -INFINITY;
 }
 
 }  // namespace

@@ -258,9 +258,11 @@ __device__ __forceinline__ int own_plan(const PromptAttnArgs &a, PromptItem *lis
         }
         list[at + i] = x;
       }
-      if (blockIdx.x == 0) a.join[tid] = PromptJoin{it.q0, it.rows, part, c > 1 ? c : 0};
+      // (a block that is cut has keys: what a row sees is bounded by `see` alone)
+      if (blockIdx.x == 0)
+        a.join[tid] = PromptJoin{it.q0, it.rows, part, c > 1 ? c : 0, it.see};
     }
-    if (blockIdx.x == 0 && tid >= items && tid < a.max_items) a.join[tid] = PromptJoin{0, 0, 0, 0};
+    if (blockIdx.x == 0 && tid >= items && tid < a.max_items) a.join[tid] = PromptJoin{};
     __syncthreads();
     return n;
   }
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           : a.hdr->items > 0;
     if (!__syncthreads_or(some)) {
       grid_dep_launch();
-      if (split && blockIdx.x == 0 && b < a.max_items) a.join[b] = PromptJoin{0, 0, 0, 0};
+      if (split && blockIdx.x == 0 && b < a.max_items) a.join[b] = PromptJoin{};
       return;
     }
   }
@@ -859,11 +861,12 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptAttnArgs a
     }
   }
   l = warp_sum(l);
-  const float inv = l != 0.f ? 1.f / l : 0.f;
+  const bool some = jn.see + (row >> lg) > 0;      // the row sees a key
+  const float inv = some ? 1.f / l : 0.f;
   const long dst = (long)(jn.q0 + (row >> lg)) * a.n_heads + (pack << lg) + (row & ((1 << lg) - 1));
   *reinterpret_cast<uint2 *>(static_cast<bf16 *>(a.out) + dst * 128 + 4 * lane) =
       make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
-  if (a.lse && lane == 0) a.lse[dst] = l != 0.f ? (top + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+  if (a.lse && lane == 0) a.lse[dst] = some ? (top + __log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // ------------------------------------------------------------------ host side
