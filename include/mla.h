@@ -87,7 +87,8 @@ enum { MLA_ROPE_INTERLEAVED = 0, MLA_ROPE_HALF = 1 };
  *     max_j |c_j| <= 127 * 2^e, q_j = round-half-even(c_j / s).  Because s is a
  *     power of two, q_j * s is exactly representable in bf16: decode attention
  *     over an int8 cache computes exactly what it computes over the bf16 rows
- *     [q * s ; k_R]. */
+ *     [q * s ; k_R].  A row whose c is not finite throughout is written with
+ *     codes 0 and a scale of NaN: its c reads back as NaN. */
 enum { MLA_CACHE_NATIVE = 0, MLA_CACHE_INT8 = 1 };
 enum { MLA_INT8_ROW_BYTES = 656 };
 

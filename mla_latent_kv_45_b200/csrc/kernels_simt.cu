@@ -197,7 +197,7 @@ __global__ void append_finish_int8(const float *xkv, int batch, int d_c, RopePar
   for (int i = threadIdx.x; i < d_c; i += blockDim.x) {
     const float c = __bfloat162float(gamma[i]) * (x[i] * inv_rms);
     x[i] = c;
-    am = fmaxf(am, fabsf(c));
+    am = fmaxf(am, isfinite(c) ? fabsf(c) : INFINITY);     // (fmaxf alone drops NaN)
   }
   am = warp_max(am);
   __syncthreads();
@@ -211,8 +211,9 @@ __global__ void append_finish_int8(const float *xkv, int batch, int d_c, RopePar
   __syncthreads();
   const float amax = amax_s;
   // amax in [2^k, 2^(k+1)): 127 * 2^(k-6) = 1.98 * 2^k, so e is k - 6 or k - 5
+  const bool finite = amax < INFINITY;      // else the row's scale is NaN, and every c read from it
   int e = 0;
-  if (amax > 0.f) {
+  if (finite && amax > 0.f) {
     e = ilogbf(amax) - 6;
     if (amax > ldexpf(127.f, e)) ++e;
   }
@@ -227,7 +228,7 @@ __global__ void append_finish_int8(const float *xkv, int batch, int d_c, RopePar
   }
   uint8_t *dst = pool + ((long)page * page_size + pos % page_size) * 656;
   for (int i = threadIdx.x; i < d_c; i += blockDim.x) {
-    const int q = max(-127, min(127, __float2int_rn(x[i] * inv_s)));
+    const int q = finite ? max(-127, min(127, __float2int_rn(x[i] * inv_s))) : 0;
     dst[i] = static_cast<uint8_t>(static_cast<int8_t>(q));
   }
   __nv_bfloat16 *kr = reinterpret_cast<__nv_bfloat16 *>(dst + d_c);
@@ -241,7 +242,8 @@ __global__ void append_finish_int8(const float *xkv, int batch, int d_c, RopePar
   }
   if (threadIdx.x < 4) {
     uint32_t *tail = reinterpret_cast<uint32_t *>(dst + d_c + 2 * rp.d_rope);   // bytes 640..655
-    tail[threadIdx.x] = threadIdx.x == 0 ? __float_as_uint(ldexpf(1.f, e)) : 0u;
+    const uint32_t s = finite ? __float_as_uint(ldexpf(1.f, e)) : 0x7fc00000u;
+    tail[threadIdx.x] = threadIdx.x == 0 ? s : 0u;
   }
 }
 

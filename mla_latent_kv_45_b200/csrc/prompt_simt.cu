@@ -288,13 +288,14 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       d[i] = (double)gm[i] * (double)c[i] * inv;
-      am = fmax(am, fabs(d[i]));
+      am = fmax(am, isfinite(d[i]) ? fabs(d[i]) : HUGE_VAL);     // (fmax alone drops NaN)
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) am = fmax(am, __shfl_xor_sync(0xffffffffu, am, o));
     // am in [2^k, 2^(k+1)): 127 * 2^(k-6) = 1.98 * 2^k, so e is k - 6 or k - 5
+    const bool finite = am < HUGE_VAL;      // else the row's scale is NaN, and every c read from it
     int e = 0;
-    if (am > 0.0) {
+    if (finite && am > 0.0) {
       e = ilogb(am) - 6;
       if (am > ldexp(127.0, e)) ++e;
     }
@@ -302,7 +303,7 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int q = max(-127, min(127, __double2int_rn(d[i] * inv_s)));
+      const int q = finite ? max(-127, min(127, __double2int_rn(d[i] * inv_s))) : 0;
       w[i >> 2] |= (uint32_t)(q & 255) << (8 * (i & 3));
     }
     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.pool) + slot * 656);
@@ -312,7 +313,8 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
       dst[32 + v0] = kp;
       dst[32 + v1] = kr;
     }
-    if (lane == 4) dst[40] = make_uint4(__float_as_uint(ldexpf(1.f, e)), 0, 0, 0);
+    if (lane == 4)
+      dst[40] = make_uint4(finite ? __float_as_uint(ldexpf(1.f, e)) : 0x7fc00000u, 0, 0, 0);
   }
 }
 
