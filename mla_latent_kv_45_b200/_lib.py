@@ -2,7 +2,8 @@
 
 The prompt calls, whose small sizes take less time than ten tensors' checks in Python, go
 through the same checks in C++ (``csrc/marshal.cpp``) first; those decline what is not
-exactly right, and the checks here then say what is wrong.
+exactly right, and the checks here then say what is wrong.  Without that module, or with one
+that was built for another torch, the checks here are the only ones.
 
 Argument marshalling only: every function here forwards torch tensors' device
 pointers and sizes to the C ABI call of the same name and raises ``MlaError``
@@ -15,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import warnings
 from typing import Optional
 
 import torch
@@ -156,12 +158,31 @@ def lib() -> ctypes.CDLL:
             if name not in ("mla_workspace_size", "mla_prompt_workspace_size",
                             "mla_status_string"):
                 getattr(L, name).restype = i
-        from . import _marshal as m
-        m.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value
-                 for f in ("mla_prompt_append", "mla_cache_gather", "mla_prompt_attn")))
-        _marshal = m
+        _marshal = _load_marshal(L)
         _lib = L
     return _lib
+
+
+def torch_build() -> str:
+    """The torch in use, as far as the binary interface of an extension goes."""
+    return (f"{torch.__version__} {torch.version.git_version} "
+            f"abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}")
+
+
+def _load_marshal(L: ctypes.CDLL):
+    """The prompt calls' checks in C++, or None."""
+    try:
+        from . import _marshal as m
+        if m.BUILT_FOR != torch_build():
+            raise ImportError(f"it was built for torch {m.BUILT_FOR}, this is {torch_build()}")
+    except (ImportError, AttributeError) as e:
+        warnings.warn("the prompt calls go through their checks in Python, which take the host "
+                      f"some 10 us a call: no extension module _marshal ({e}); "
+                      "`python -m mla_latent_kv_45_b200.build` builds it")
+        return None
+    m.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value
+             for f in ("mla_prompt_append", "mla_cache_gather", "mla_prompt_attn")))
+    return m
 
 
 def status_string(status: int) -> str:
@@ -357,7 +378,7 @@ def mla_prompt_append(dims: Dims, cache: PagedCache, x, gamma, cu_tokens, ctx_le
     """
     fn = "mla_prompt_append"
     lib()
-    if (s := _address(stream)) is not False:
+    if _marshal is not None and (s := _address(stream)) is not False:
         st = _marshal.append(dims.c(), cache.pool, cache.block_table, x, gamma, cu_tokens,
                              ctx_lens, q_rope, q_out, ws, s)
         if st is not None:
@@ -388,7 +409,7 @@ def mla_cache_gather(dims: Dims, cache: PagedCache, cu_rows, first_rows, rows,
     packed at cu_rows ``[batch + 1]``; int8 rows come back as the values they hold."""
     fn = "mla_cache_gather"
     lib()
-    if (s := _address(stream)) is not False:
+    if _marshal is not None and (s := _address(stream)) is not False:
         st = _marshal.gather(dims.c(), cache.pool, cache.block_table, cu_rows, first_rows, rows,
                              ws, s)
         if st is not None:
@@ -416,7 +437,7 @@ def mla_prompt_attn(dims: Dims, q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, o
     """
     fn = "mla_prompt_attn"
     lib()
-    if (s := _address(stream)) is not False:
+    if _marshal is not None and (s := _address(stream)) is not False:
         st = _marshal.attn(dims.c(), q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, out, lse, ws, s)
         if st is not None:
             return _ok(fn, st)

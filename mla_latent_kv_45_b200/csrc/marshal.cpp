@@ -269,4 +269,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
+// The module reads tensors through the headers of the torch it was compiled against and is
+// used with no other: BUILT_FOR (_lib.torch_build) is compared before bind is called.
+PyMODINIT_FUNC PyInit__marshal() {
+  PyObject *m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "BUILT_FOR", MLA_BUILT_FOR)) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
