@@ -43,7 +43,7 @@
 
 #include "api_checks.h"
 #include "prompt.h"
-#include "ptx.cuh"
+#include "prompt_ptx.cuh"
 
 namespace mla {
 namespace sm100 {
