@@ -110,9 +110,13 @@ class PromptLayer:
     Weights as for ``DecodeLayer``; buffers for ``tokens`` new tokens of ``batch``
     sequences that have ``rows`` cached rows in all once the chunk is appended.
     Prompts may come in one chunk or in several: a chunk attends over everything its
-    sequences have in the cache.  The same cache then serves ``DecodeLayer``.
+    sequences have in the cache.  The same cache then serves ``DecodeLayer``.  The weights
+    are laid out when the layer is made (W_DKV and W_KR are copied, the others are views): make
+    another after changing them.  Nothing is recorded for a backward pass.
     """
 
+    @torch.inference_mode(False)      # buffers that later steps may write in either mode
+    @torch.no_grad()
     def __init__(self, dims: L.Dims, weights: dict, batch: int, tokens: int, rows: int,
                  device="cuda"):
         if min(batch, tokens, rows) < 1:
@@ -145,6 +149,7 @@ class PromptLayer:
         self.out = (self.o.view(tokens, -1) if self.w_o is None
                     else new(tokens, self.w_o.shape[1]))
 
+    @torch.no_grad()
     def step(self, cache: L.PagedCache, h: torch.Tensor, cu_tokens: torch.Tensor,
              ctx_lens: Optional[torch.Tensor], cu_rows: torch.Tensor, stream=None) -> torch.Tensor:
         """The layer output of the tokens ``h`` ``[tokens, d_model]``.

@@ -1,0 +1,74 @@
+"""PromptLayer as a program uses it: weights that are parameters, grad and inference modes."""
+
+import pytest
+import torch
+
+from mla_latent_kv_45_b200 import _lib as L
+from mla_latent_kv_45_b200 import build, synth
+from mla_latent_kv_45_b200.layer import DecodeLayer, PromptLayer
+from mla_testlib import dev, dev_weights, lib_dims
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build.build()
+    L.lib()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+SIZES = {
+    "fp32": synth.TINY,
+    "bf16": synth.reduced(synth.V2_STEP128, "prompt", 94, 1, 0, 0, d_model=1024, d_q=512),
+}
+N = 20
+
+
+def case(name):
+    wl = SIZES[name]
+    dims, Wd = lib_dims(wl), dev_weights(synth.make_weights(wl), wl)
+    ps = wl.page_size
+    pages = -(-(N + 1) // ps)
+    pool = torch.zeros(pages, ps, wl.row, dtype=dims.torch_dtype, device="cuda")
+    cache = L.PagedCache(pool, i32([list(range(pages))]), None)
+    return wl, dims, Wd, cache, dev(synth.make_hidden(wl, n=N), wl)
+
+
+def prompt(dims, W, cache, h):
+    layer = PromptLayer(dims, W, 1, N, N)
+    out = layer.step(cache, h, i32([0, N]), None, i32([0, N])).clone()
+    assert layer.device_error() == 0
+    return layer, out
+
+
+@pytest.mark.parametrize("name", SIZES)
+def test_weights_and_inputs_that_require_a_gradient(name):
+    """The layer takes a model's parameters as DecodeLayer does, and records nothing."""
+    wl, dims, Wd, cache, h = case(name)
+    _, want = prompt(dims, Wd, cache, h)
+    params = {k: None if v is None else torch.nn.Parameter(v.clone()) for k, v in Wd.items()}
+    layer, out = prompt(dims, params, cache, h.clone().requires_grad_())
+    assert torch.equal(out, want) and not layer.step(cache, h, i32([0, N]), None, i32([0, N])).requires_grad
+    g = layer.capture(cache, h, i32([0, N]), None, i32([0, N]))
+    layer.out.zero_()
+    assert torch.equal(g.replay(), want)
+    cache.seq_lens = i32([N + 1])
+    dec = DecodeLayer(dims, params, 1)
+    assert torch.isfinite(dec.step(cache, h[-1:].contiguous(), i32([N]))).all()
+
+
+@pytest.mark.parametrize("made,used", [(False, True), (True, False), (True, True)])
+def test_inference_mode(made, used):
+    wl, dims, Wd, cache, h = case("bf16")
+    _, want = prompt(dims, Wd, cache, h)
+    with torch.inference_mode(made):
+        layer = PromptLayer(dims, {k: None if v is None else v.clone() for k, v in Wd.items()}, 1, N, N)
+    with torch.inference_mode(used):
+        out = layer.step(cache, h, i32([0, N]), None, i32([0, N]))
+        assert torch.equal(out, want)
+    assert layer.device_error() == 0
