@@ -189,8 +189,11 @@ class PromptLayer:
         return StepGraph(lambda s: self.step(cache, h, cu_tokens, ctx_lens, cu_rows, s), self.out)
 
     def device_error(self) -> int:
-        """Synchronises; returns the device status of the workspace."""
-        return L.mla_get_device_error(self.ws)
+        """Waits for the layer's device (a step or a replay may be on any stream of it); returns
+        the device status of the workspace."""
+        with torch.cuda.device(self.ws.device):
+            torch.cuda.synchronize()
+            return L.mla_get_device_error(self.ws)
 
 
 class StepGraph:

@@ -72,3 +72,23 @@ def test_inference_mode(made, used):
         out = layer.step(cache, h, i32([0, N]), None, i32([0, N]))
         assert torch.equal(out, want)
     assert layer.device_error() == 0
+
+
+def test_error_of_a_step_on_another_stream():
+    """The status is that of all steps, those that other streams have not come to as well."""
+    wl, dims, Wd, cache, h = case("fp32")
+    layer = PromptLayer(dims, Wd, 1, N, N)
+    side = torch.cuda.Stream()
+    cu, bad = i32([0, N]), i32([0, N + 1])
+    torch.cuda.synchronize()
+    for offsets, want in ((bad, 6), (cu, 0), (bad, 6)):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)      # about a tenth of a second
+        layer.step(cache, h, cu, None, offsets, side)
+        assert layer.device_error() == want
+    g = layer.capture(cache, h, cu, None, bad)
+    assert layer.device_error() == 6
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        g.replay()
+    assert layer.device_error() == 6
