@@ -135,7 +135,8 @@ class PromptLayer:
         self.w_o = None if w.get("W_O") is None else w["W_O"].T
         self.gamma = w["gamma"]
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        L.mla_workspace_init(self.ws)
+        with torch.cuda.device(self.ws.device):     # (the current stream is the layer's device's)
+            L.mla_workspace_init(self.ws)
         new = lambda *s: torch.empty(*s, dtype=dt, device=device)  # noqa: E731
         # the projections of the cache row stay in fp32 until they are normalised and
         # rotated, as in the decode step
@@ -184,9 +185,11 @@ class PromptLayer:
     def capture(self, cache: L.PagedCache, h: torch.Tensor, cu_tokens: torch.Tensor,
                 ctx_lens: Optional[torch.Tensor], cu_rows: torch.Tensor) -> "StepGraph":
         """The chunk over these buffers as a CUDA graph; lengths are read at replay."""
-        self.step(cache, h, cu_tokens, ctx_lens, cu_rows)
-        torch.cuda.synchronize()
-        return StepGraph(lambda s: self.step(cache, h, cu_tokens, ctx_lens, cu_rows, s), self.out)
+        with torch.cuda.device(self.ws.device):
+            self.step(cache, h, cu_tokens, ctx_lens, cu_rows)
+            torch.cuda.synchronize()
+            return StepGraph(lambda s: self.step(cache, h, cu_tokens, ctx_lens, cu_rows, s),
+                             self.out)
 
     def device_error(self) -> int:
         """Waits for the layer's device (a step or a replay may be on any stream of it); returns

@@ -92,3 +92,39 @@ def test_error_of_a_step_on_another_stream():
         torch.cuda._sleep(200_000_000)
         g.replay()
     assert layer.device_error() == 6
+
+
+def test_what_uses_the_current_device_does_so_on_the_layers(monkeypatch):
+    """One GPU stands for several here: the layer makes its own device current wherever it or
+    the binding asks for the current stream."""
+    wl, dims, Wd, cache, h = case("fp32")
+    inside = []
+
+    class Device(torch.cuda.device):
+        def __enter__(self):
+            inside.append(self.idx)
+            return super().__enter__()
+
+        def __exit__(self, *a):
+            inside.pop()
+            return super().__exit__(*a)
+
+    seen = []
+
+    def noted(name, f):
+        def g(*a, **k):
+            seen.append((name, inside[-1:] == [0]))
+            return f(*a, **k)
+        return g
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(L, "mla_workspace_init", noted("init", L.mla_workspace_init))
+    monkeypatch.setattr(L, "mla_get_device_error", noted("error", L.mla_get_device_error))
+    monkeypatch.setattr(torch.cuda, "synchronize", noted("synchronize", torch.cuda.synchronize))
+    monkeypatch.setattr(torch.cuda, "CUDAGraph", noted("graph", torch.cuda.CUDAGraph))
+    layer = PromptLayer(dims, Wd, 1, N, N)
+    g = layer.capture(cache, h, i32([0, N]), None, i32([0, N]))
+    g.replay()
+    assert layer.device_error() == 0
+    assert {n for n, _ in seen} == {"init", "error", "synchronize", "graph"}
+    assert all(ok for _, ok in seen), seen
