@@ -268,8 +268,9 @@ size_t mla_prompt_workspace_size(const mla_dims *dims, int batch, int n_tokens);
  * for none; q_rope, q_out: [n_tokens][n_heads][d_rope], both or neither (NULL);
  * q_out may be q_rope itself, but may not overlap it otherwise.
  * seq_lens is not read or changed, so it may be NULL in `cache`.  A row whose
- * position has no page is not written and sets the error word (its queries are
- * rotated).  Two tokens of one call may not map to the same slot. */
+ * position has no page is not written and sets the error word; its queries are
+ * rotated all the same where the position is in [0, 2^31), and keep what q_out held
+ * where it is not.  Two tokens of one call may not map to the same slot. */
 mla_status mla_prompt_append(const mla_dims *dims, const mla_paged_cache *cache, int batch,
                              int n_tokens, const void *x, int x_dtype, int64_t x_stride,
                              const void *gamma, const int32_t *cu_tokens, const int32_t *ctx_lens,
