@@ -223,7 +223,8 @@ mla_status mla_unabsorb_out(const mla_dims *dims, int batch, const void *z, cons
  * packed without padding: the tokens of sequence b are [cu[b], cu[b+1]) of the
  * packed tensors, with cu an ascending int32 device array of batch + 1 offsets
  * (sequences may be empty).  Packed rows outside [cu[0], cu[batch]) reach no
- * result and are not written.  Their supported shapes are those of the other calls, and
+ * result and are not written; offsets that do not ascend or that leave the packed
+ * tensors set the error word.  Their supported shapes are those of the other calls, and
  * with MLA_BF16 any n_heads <= 256 (heads shared out over devices) and any
  * page_size >= 1.
  *
