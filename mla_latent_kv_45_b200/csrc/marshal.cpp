@@ -104,6 +104,19 @@ PyObject *decline() {
   Py_RETURN_NONE;
 }
 
+// The interpreter's lock is given up while this lives, and is back before an exception of the
+// library is caught.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked &) = delete;
+  Unlocked &operator=(const Unlocked &) = delete;
+
+ private:
+  PyThreadState *state_;
+};
+
 // No C++ exception leaves a call from Python.
 template <class F>
 PyObject *guarded(F &&f) {
@@ -154,10 +167,11 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int64_t xs = x->stride(0);
     const int32_t *cup = ints(cu), *ctxp = ints(ctx);
     mla_status st;
-    Py_BEGIN_ALLOW_THREADS
-    st = call_append(&d, &c, (int)batch, (int)tokens, xp, xd, xs, gp, cup, ctxp,
-                     with_q ? &q : nullptr, with_q ? &qo : nullptr, ws, bytes, s);
-    Py_END_ALLOW_THREADS
+    {
+      Unlocked unlocked;
+      st = call_append(&d, &c, (int)batch, (int)tokens, xp, xd, xs, gp, cup, ctxp,
+                       with_q ? &q : nullptr, with_q ? &qo : nullptr, ws, bytes, s);
+    }
     return PyLong_FromLong(st);
   });
 }
@@ -187,9 +201,10 @@ PyObject *py_gather(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int32_t *cup = ints(cu), *fp = ints(first);
     void *rp = rows->data_ptr();
     mla_status st;
-    Py_BEGIN_ALLOW_THREADS
-    st = call_gather(&d, &c, (int)batch, n_rows, cup, fp, rp, ws, bytes, s);
-    Py_END_ALLOW_THREADS
+    {
+      Unlocked unlocked;
+      st = call_gather(&d, &c, (int)batch, n_rows, cup, fp, rp, ws, bytes, s);
+    }
     return PyLong_FromLong(st);
   });
 }
@@ -228,10 +243,11 @@ PyObject *py_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *op = out->data_ptr();
     float *lp = lse ? static_cast<float *>(lse->data_ptr()) : nullptr;
     mla_status st;
-    Py_BEGIN_ALLOW_THREADS
-    st = call_attn(&d, (int)(off - 1), (int)n_q, (int)n_k, (int)kv, &hq, &hr, &hk, krp, krs, &hv,
-                   cqp, ckp, op, lp, ws, bytes, s);
-    Py_END_ALLOW_THREADS
+    {
+      Unlocked unlocked;
+      st = call_attn(&d, (int)(off - 1), (int)n_q, (int)n_k, (int)kv, &hq, &hr, &hk, krp, krs, &hv,
+                     cqp, ckp, op, lp, ws, bytes, s);
+    }
     return PyLong_FromLong(st);
   });
 }
