@@ -74,8 +74,10 @@ struct PromptPlanHeader {
   unsigned done;
 };
 
+// Multiprocessors of a B200, where a rule counts them.
+constexpr int kPromptSms = 148;
 // Partial results of a call, one for each CTA at most.
-constexpr int kPromptParts = 148;
+constexpr int kPromptParts = kPromptSms;
 
 struct PromptPlanArgs {
   const int32_t *cu_q, *cu_k;

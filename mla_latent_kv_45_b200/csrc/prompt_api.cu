@@ -47,9 +47,12 @@ int least_tile_tokens(const mla_dims &d) {
 // Tokens up to which a sequence goes to the kernel for few rows (bf16; 0: that kernel is not
 // launched).  The lengths are on the device only, so the average decides whether it
 // is worth a launch (100 sequences of 0-8 tokens, 128 heads: 79 us, 223 without it).  Few
-// blocks whose keys may be long are cut into pieces instead: one token over 1000, 1500
-// and 1990 rows takes 12.8, 16.8 and 20.8 us here and 18.5, 16.3 and 18.0 there with 16 heads,
-// 13.0, 17.1 and 21.2 here and 18.9, 21.1 and 24.0 there with 64.
+// blocks whose keys may be long are cut into pieces instead, from twice the keys on that
+// cutting starts at.  The more heads, the later that pays (a block has fewer pieces): one
+// token over 1200, 1600, 2000, 2600 and 3200 rows takes with 16 heads 14.3, 17.6, 20.8, 25.5 and
+// 30.1 us here and 15.5, 15.4, 16.2, 17.8 and 18.4 cut, with 32 heads 14.6, 17.7, 21.0, 25.9 and
+// 30.3 here and 15.8, 16.1, 18.0, 20.4 and 21.3 cut, with 64 heads 14.5, 17.7, 21.0, 25.9 and
+// 30.6 here and 19.0, 21.1, 23.9, 28.1 and 31.3 cut.
 int few_tokens(const mla_dims &d, int rep, int batch, int n_q, int n_k, long max_items) {
   if (d.dtype != MLA_BF16 || rep > kPromptFewRows) return 0;
   const int most = kPromptFewRows / rep;

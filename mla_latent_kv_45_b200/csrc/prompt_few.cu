@@ -288,8 +288,13 @@ cudaError_t launch_prompt_few(const PromptAttnArgs &a, cudaStream_t s) {
   // another's first loads are on their way.  (1 token over 4001 rows, 128 heads: 50 us
   // and 83; 64 x 1 token over 100-2000 rows, 8 key heads: 64 and 73; 52 x 1-2 tokens over 95
   // rows, 128 heads: 172 and 88; 64 x 1-16 tokens over 100-200 rows: 270 and 153.)
+  // The host knows the keys' average alone, and the border lies where lengths differ: 64 x 1
+  // token over 20 to twice the average, 16 heads, takes 47.9 us and 40.0 at an average of
+  // 300, 62.2 and 57.5 at 512, 67.6 and 71.7 at 600, 84 and 92 at 830; in 4 key heads 21.8 and
+  // 32.8 at 512; 61 over 60 rows beside 3 over 11581 127 and 274.  Equal lengths would go on with
+  // two warps: 61.6 and 49.4 at 512 each, 98 and 88 at 1024.
   const long ctas = (long)a.batch * a.n_kv_heads;
-  return ctas <= 148 || a.n_k >= 512L * a.batch ? launch<8, 2, 1>(a, s) : launch<2, 2, 4>(a, s);
+  return ctas <= kPromptSms || a.n_k >= 512L * a.batch ? launch<8, 2, 1>(a, s) : launch<2, 2, 4>(a, s);
 }
 
 }  // namespace mla

@@ -286,8 +286,10 @@ __global__ void prompt_append_bf16(PromptAppendArgs a, const __grid_constant__ R
     }
   } else {
     // In 64 bits: a code is a rounding of c / 2^e, and a 32-bit c next to a
-    // border between two codes would fall on the wrong side of it.  About 50
-    // such operations a lane, far below the time the row's bytes take.
+    // border between two codes would fall on the wrong side of it.  Some 50 such
+    // operations a lane, which cost more than the row's bytes: 8,192 rows take 14.9 us
+    // without queries and 53.8 with those of 128 heads, bf16 rows 10.0 and 46.1; 65,536 rows
+    // 104 us, bf16 rows 66.
     double ss = 0.0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) ss += (double)c[i] * (double)c[i];
@@ -369,7 +371,8 @@ __device__ __forceinline__ uint4 codes8(const uint2 &in, float s) {
 
 constexpr int kGatherRows = 2;  // rows of a warp, all asked for before the first is written
 
-// One warp two rows (one or four: 5 % slower for bf16 or for int8 rows): a pass of reads and writes, bound by the bytes.
+// One warp two rows (one or four: 5 % slower for bf16 or for int8 rows): a pass of reads and
+// writes, bound by the bytes.
 template <bool kI8>
 __global__ void gather_bf16(GatherArgs a) {
   const int lane = threadIdx.x & 31;

@@ -37,8 +37,8 @@
 // from shared memory in it and TMA writes 50 KB there, which at 128 bytes a cycle is
 // 1920 cycles; the softmax of a tile is a chain of about 1830.  An item costs about
 // 6000 cycles beside its steps (the tile with the earlier rows waits for the other).
-// 8192 tokens, 128 heads: 2.01 ms by itself (1370 TFLOP/s, 84 % of the measured
-// matrix rate), 2.3 ms back to back, where the power limit lowers the clock.
+// 8192 tokens, 128 heads: 2.03 ms by itself (1350 TFLOP/s, 83 % of the measured
+// matrix rate), 2.36 ms back to back, where the power limit lowers the clock.
 #include <cuda.h>
 
 #include "api_checks.h"
@@ -143,7 +143,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // 8 words of P: the weights 2^(scale v - m) of 16 columns, added to the row sum
-// unrounded.  (Part of them on the FMA pipe instead of the special-function unit
+// unrounded.  They are rounded to bf16 because both operands of the product with V have one
+// type and V is bf16: each is off by 2^-8 of itself at most, which leaves the result
+// 1.2-1.4x as far from 64 bits as weights in 32 bits do (2.0e-3 against 1.5e-3 for 8192 tokens,
+// most of both the rounding of the result).  A second bf16 term for the remainder would
+// double the product, 40 % of a step's MMAs.  (Part of them on the FMA pipe instead of the special-function unit
 // made the kernel slower at every share: it is short of issue slots, not of that unit.)
 __device__ __forceinline__ void weights16(const float *v, uint64_t scale2, uint64_t base2,
                                           uint64_t (&sum)[2], uint32_t *p) {
