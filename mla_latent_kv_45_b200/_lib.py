@@ -82,19 +82,26 @@ class Dims:
     softmax_scale: float = 0.0
     cache_format: int = MLA_CACHE_NATIVE
 
+    __slots__ = ("_kept", "__dict__", "__weakref__")     # (_kept is no field and not in __dict__)
+
     def __setattr__(self, name, value):
-        self.__dict__.pop("_c", None)
-        self.__dict__[name] = value
+        object.__setattr__(self, name, value)
+        if name != "_kept":
+            object.__setattr__(self, "_kept", None)
 
     def c(self) -> _Dims:
-        """The C struct (made once; setting a field drops it)."""
-        c = self.__dict__.get("_c")
-        if c is None:
-            c = _Dims(self.n_heads, self.d_c, self.d_rope, self.d_nope, self.d_v, self.page_size,
-                      self.dtype, self.rope_layout, self.rope_base, self.rms_eps,
-                      self.softmax_scale, self.cache_format)
-            self.__dict__["_c"] = c
-        return c
+        """A C struct of the fields."""
+        return _Dims(self.n_heads, self.d_c, self.d_rope, self.d_nope, self.d_v, self.page_size,
+                     self.dtype, self.rope_layout, self.rope_base, self.rms_eps,
+                     self.softmax_scale, self.cache_format)
+
+    def kept(self) -> _Dims:
+        """The C struct for calls that only read it, made once; setting a field drops it."""
+        k = self._kept
+        if k is None:
+            k = self.c()
+            object.__setattr__(self, "_kept", k)
+        return k
 
     @property
     def torch_dtype(self):
@@ -379,7 +386,7 @@ def mla_prompt_append(dims: Dims, cache: PagedCache, x, gamma, cu_tokens, ctx_le
     fn = "mla_prompt_append"
     lib()
     if _marshal is not None and (s := _address(stream)) is not False:
-        st = _marshal.append(dims.c(), cache.pool, cache.block_table, x, gamma, cu_tokens,
+        st = _marshal.append(dims.kept(), cache.pool, cache.block_table, x, gamma, cu_tokens,
                              ctx_lens, q_rope, q_out, ws, s)
         if st is not None:
             return _ok(fn, st)
@@ -410,7 +417,7 @@ def mla_cache_gather(dims: Dims, cache: PagedCache, cu_rows, first_rows, rows,
     fn = "mla_cache_gather"
     lib()
     if _marshal is not None and (s := _address(stream)) is not False:
-        st = _marshal.gather(dims.c(), cache.pool, cache.block_table, cu_rows, first_rows, rows,
+        st = _marshal.gather(dims.kept(), cache.pool, cache.block_table, cu_rows, first_rows, rows,
                              ws, s)
         if st is not None:
             return _ok(fn, st)
@@ -438,7 +445,8 @@ def mla_prompt_attn(dims: Dims, q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, o
     fn = "mla_prompt_attn"
     lib()
     if _marshal is not None and (s := _address(stream)) is not False:
-        st = _marshal.attn(dims.c(), q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, out, lse, ws, s)
+        st = _marshal.attn(dims.kept(), q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, out, lse,
+                           ws, s)
         if st is not None:
             return _ok(fn, st)
     dt, i32, H = dims.torch_dtype, torch.int32, dims.n_heads
