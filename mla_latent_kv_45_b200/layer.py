@@ -159,7 +159,9 @@ class PromptLayer:
         follow the ``ctx_lens[b]`` rows (None: no rows) that it has in the cache;
         ``cu_rows`` are the offsets of all its rows, cu_rows[b+1] - cu_rows[b] =
         ctx_lens[b] + cu_tokens[b+1] - cu_tokens[b] (int32 device tensors, all read
-        on the device).  cache.seq_lens is not read.
+        on the device).  cache.seq_lens is not read.  Output rows of tokens that no sequence
+        has mean nothing.  The result is the layer's buffer; the inputs have to stay as they are
+        until ``stream`` (None: the current one) has come past the step.
         """
         if h.shape[0] != self.tokens:     # (the products would resize their outputs)
             raise ValueError(f"h has {h.shape[0]} tokens, the buffers are for {self.tokens}")
