@@ -147,8 +147,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // type and V is bf16: each is off by 2^-8 of itself at most, which leaves the result
 // 1.2-1.4x as far from 64 bits as weights in 32 bits do (2.0e-3 against 1.5e-3 for 8192 tokens,
 // most of both the rounding of the result).  A second bf16 term for the remainder would
-// double the product, 40 % of a step's MMAs.  (Part of them on the FMA pipe instead of the special-function unit
-// made the kernel slower at every share: it is short of issue slots, not of that unit.)
+// double the product, 40 % of a step's MMAs.  (Part of the exponentials on the FMA pipe
+// instead of the special-function unit made the kernel slower at every share: it is short
+// of issue slots, not of that unit.)
 __device__ __forceinline__ void weights16(const float *v, uint64_t scale2, uint64_t base2,
                                           uint64_t (&sum)[2], uint32_t *p) {
 #pragma unroll
